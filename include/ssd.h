@@ -55,8 +55,10 @@ typedef enum {
 } ssd_status;
 
 /* Element types: weights are SSD_BF16 or SSD_FP16; the context's KV cache is
- * always fp32; the standalone attention also accepts 16-bit caches. */
-typedef enum { SSD_BF16 = 0, SSD_FP16 = 1, SSD_F32 = 2 } ssd_dtype;
+ * always fp32; the standalone attention also accepts 16-bit caches.  SSD_I8
+ * (codes in [-127, 127]) and SSD_E4M3 are the code types of the 8-bit cache
+ * (ssd_kv8_cache) only. */
+typedef enum { SSD_BF16 = 0, SSD_FP16 = 1, SSD_F32 = 2, SSD_I8 = 3, SSD_E4M3 = 4 } ssd_dtype;
 
 /* Shape of the decoder.  head_dim must be 64 or 128; n_q_heads a multiple of
  * n_kv_heads; d_model a multiple of 64, ffn of 16; n_layers <= 128.
@@ -335,7 +337,9 @@ void ssd_attn_ring_rule(int ntile, int S, int WQ, int* R, int* WK);
 
 /* sizeof of the ABI's structs, for bindings to check their mirrors: out[0]
  * ssd_model_config, out[1] ssd_policy, out[2] ssd_stats, out[3]
- * ssd_attention_args (n <= 4 entries written).  Host only. */
+ * ssd_attention_args, out[4] ssd_cycle_record, out[5] ssd_kv8_cache, out[6]
+ * ssd_kv8_rows, out[7] ssd_kv8_attention_args, out[8] ssd_kv8_evict_args (the
+ * first n entries are written).  Host only. */
 void ssd_abi_sizes(size_t* out, int n);
 
 /* The host planners alone (no context, no GPU).  ssd_plan_tree: the DyTC
@@ -466,6 +470,135 @@ ssd_status ssd_attention(const ssd_attention_args* args, void* scratch, size_t s
  * the array and each overwrites it: calls that overlap on the GPU (other
  * streams, other threads) race and must be serialised by the caller. */
 ssd_status ssd_attention_noalloc(const ssd_attention_args* args, void* cuda_stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit KV cache: a paged cache like the one ssd_attention reads, held as
+ * 8-bit codes with one fp32 scale for each block of tokens and KV head, the
+ * attention over it, the weight that its slots draw, and eviction by that
+ * weight.  Long contexts at batch 1 are bounded by the cache's bytes; this
+ * one is a quarter of an fp32 cache's.  The pages have no counterpart.
+ *
+ * Every call works on one layer, is asynchronous on `cuda_stream`, allocates
+ * nothing and can be captured into a CUDA graph (the numbers in the argument
+ * structs are then the graph's).  Buffers belong to the current device.  All
+ * calls on one cache that overlap on the GPU must be ordered by the caller
+ * unless none of them writes it.
+ *
+ *   k, v             device, one byte codes [n_layers][pool_pages][n_kv_heads][64][head_dim], 16-byte aligned
+ *   k_scale, v_scale device fp32 [n_layers][pool_pages][n_kv_heads][64 / block_tokens]
+ *   block_table      device int32 [n_pages]: logical page -> physical page of the pool
+ *   dtype            SSD_I8 or SSD_E4M3;  block_tokens 16, 32 or 64;  head_dim 64 or 128
+ *
+ * A slot's value is code * scale of its block.  A block is quantised with
+ *   s = amax / qmax        amax = largest finite magnitude, qmax = 127 or 448;
+ *                          below 2^-126 s becomes 0 (all codes 0)
+ *   code = x * (1 / s)     rounded to the nearest code, ties to even, clamped
+ *                          to +-qmax; every operation in fp32, rounded once
+ * so a value is off by at most s / 2 (int8) or 2^-4 of itself (e4m3 above
+ * 2^-6 s).  NaN is stored as 0, an infinity as +-qmax.
+ * A block-table entry outside [0, pool_pages) names no page: its slots are
+ * seen by nobody, read as zero, and what is appended to them is dropped. */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  int n_pages, pool_pages, layer, n_kv_heads, head_dim, dtype, block_tokens;
+} ssd_kv8_cache;
+
+/* Rows of K and V: [rows][n_kv_heads * head_dim], ld_k / ld_v elements apart,
+ * dtype SSD_F32, SSD_BF16 or SSD_FP16, for slots first .. first + rows - 1.
+ * Both matrices 16-byte aligned, rows a multiple of 16 bytes apart. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t ld_k, ld_v;
+  int dtype, first, rows;
+} ssd_kv8_rows;
+
+/* Quantise rows (K with RoPE applied) into slots first .. first + rows - 1.
+ * Blocks that start in this range get a scale of their own.  A block whose
+ * first slots lie before `first` keeps them: its scale becomes the larger of
+ * its old one and the new rows', and their codes are rounded again when it
+ * grows.  Slots of the last block past the new rows hold no token afterwards.
+ * Errors: INVALID_ARG (bad descriptor, alignment or stride; rows < 1; a slot
+ * past the block table). */
+ssd_status ssd_kv8_append(const ssd_kv8_cache* cache, const ssd_kv8_rows* rows, void* cuda_stream);
+
+/* The values of slots first .. first + rows - 1, written to rows->k and
+ * rows->v (fp32 code * scale, rounded to dtype).  Errors as ssd_kv8_append. */
+ssd_status ssd_kv8_read(const ssd_kv8_cache* cache, const ssd_kv8_rows* rows, void* cuda_stream);
+
+/* Attention of up to 64 rows, with the visibility rule of ssd_attention: row
+ * r sees slots [0, prefix) and base + e for every bit e < rows set in
+ * mask[r] (a slot that both name counts once).  Query head h reads KV head
+ * h / (n_q_heads / n_kv_heads).
+ *   q    device [rows][n_q_heads * head_dim], RoPE applied, ld_q elements apart
+ *   out  device, the same shape, ld_out apart
+ *   lse  device fp32 [rows][n_q_heads] or NULL: the log of the sum of exp of each row's scores
+ *   dtype of q and out: SSD_F32, SSD_BF16 or SSD_FP16; 16-byte aligned, rows a multiple of 16 bytes apart
+ *   scores are scale * q.k (scale > 0), with softcap > 0 then softcap * tanh(score / softcap)
+ * Sums and softmax statistics are fp32; an fp32 q is not rounded below 22
+ * bits.  A row that sees no slot gets zeros and lse -inf; slots that a row
+ * does not see may hold anything, those past every row's sight need never
+ * have been written.  Errors: INVALID_ARG (bad descriptor, pointer,
+ * alignment or stride, rows not in 1..64, n_q_heads not a multiple of
+ * n_kv_heads, a slot past the block table, scale or softcap out of range);
+ * CAPACITY (scratch too small). */
+typedef struct {
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t ld_q, ld_out;
+  int dtype, n_q_heads, rows, prefix, base;
+  float scale, softcap;
+  uint64_t mask[64];
+} ssd_kv8_attention_args;
+
+/* Device scratch that ssd_kv8_attention needs for these arguments (pointers
+ * must be valid, out is not looked at); 0 for arguments that it rejects. */
+size_t ssd_kv8_attention_scratch_bytes(const ssd_kv8_cache* cache, const ssd_kv8_attention_args* args);
+/* scratch: 256-byte aligned; its contents need no set-up; not shared by
+ * calls (or replays of graphs) that overlap on the GPU. */
+ssd_status ssd_kv8_attention(const ssd_kv8_cache* cache, const ssd_kv8_attention_args* args, void* scratch,
+                             size_t scratch_bytes, void* cuda_stream);
+
+/* Accumulated attention weight: for every KV head h and slot j in
+ * [0, max(prefix, base + rows))
+ *   weight_out[h][j] = weight_in[h][j] + sum of exp(score - lse) over the rows
+ *                      r of row_set that see j and the query heads of h
+ * with args as for ssd_kv8_attention and args->lse what it returned (out is
+ * not used).  A verify pass's rejected rows are left out of row_set.
+ * weight_in and weight_out: device fp32 [n_kv_heads], ld_weight elements
+ * apart; they may be the same; weight_in NULL counts as zeros.  Errors:
+ * INVALID_ARG (as the attention; lse NULL; ld_weight too small). */
+ssd_status ssd_kv8_weights(const ssd_kv8_cache* cache, const ssd_kv8_attention_args* args, uint64_t row_set,
+                           const float* weight_in, float* weight_out, int64_t ld_weight, void* cuda_stream);
+
+/* Eviction.  Of slots [0, n) every KV head keeps the last `recent` and the
+ * keep - recent heaviest of the others (by weight[h][j]; the lowest slot
+ * among equal ones; NaN counts as the lightest), and they move, in slot
+ * order, to slots [0, keep) of `to`, whose blocks are quantised anew from the
+ * values that `from` holds.  K is stored with RoPE applied, so slots keep
+ * their positions; the heads' slots differ from then on.
+ *   weight       device fp32 [n_kv_heads], ld_weight elements apart
+ *   index        device int32 [n_kv_heads][keep]: receives the kept slots
+ *   kept_weight  device fp32 [n_kv_heads][keep] or NULL: receives their weights
+ * `to` has the heads of `from` (its dtype and block_tokens may differ), and
+ * its first ceil(keep / 64) pages must be none of from's.  Errors:
+ * INVALID_ARG (bad descriptor or pointer, shapes that differ, not
+ * 0 <= recent <= keep <= n, keep < 1, n past the block table); CAPACITY
+ * (keep past to's block table). */
+typedef struct {
+  const float* weight;
+  int64_t ld_weight;
+  int32_t* index;
+  float* kept_weight;
+  int n, keep, recent;
+} ssd_kv8_evict_args;
+ssd_status ssd_kv8_evict(const ssd_kv8_cache* from, const ssd_kv8_cache* to, const ssd_kv8_evict_args* args,
+                         void* cuda_stream);
 
 const char* ssd_last_error(const ssd_ctx* ctx);
 const char* ssd_status_string(ssd_status s);

@@ -27,5 +27,7 @@ Modules:
               speculative cycles, greedy acceptance + KV rollback, DyTC
               routing + EMA, horizontal and vertical cascade baselines
   clasp.py    CLaSp dynamic-programming skip search + brute force
+  kv8.py      8-bit KV cache: quantisation, attention, attention weights,
+              eviction
   latency.py  latency model fit and cascade depth rules of the scheduler
 """

@@ -33,7 +33,8 @@ EXPORTS = ("ssd_workspace_bytes", "ssd_create", "ssd_weight_count", "ssd_load_we
            "ssd_calibrate_latency", "ssd_set_latency_model", "ssd_fit_latency", "ssd_get_level_costs",
            "ssd_cascade_depth", "ssd_plan_tree", "ssd_plan_hcascade", "ssd_abi_sizes", "ssd_attention_noalloc",
            "ssd_get_cycle_log", "ssd_set_ema", "ssd_get_dp_table", "ssd_streamk_split",
-           "ssd_gemv_warps", "ssd_attn_ring_rule")
+           "ssd_gemv_warps", "ssd_attn_ring_rule", "ssd_kv8_append", "ssd_kv8_read", "ssd_kv8_attention_scratch_bytes",
+           "ssd_kv8_attention", "ssd_kv8_weights", "ssd_kv8_evict")
 
 
 class ModelConfigC(ctypes.Structure):
@@ -75,6 +76,31 @@ class CycleRecordC(ctypes.Structure):
                 ("n_acc", ctypes.c_int32), ("bonus", ctypes.c_int32), ("tokens", ctypes.c_int32 * 64),
                 ("parents", ctypes.c_int32 * 64), ("argmax", ctypes.c_int32 * 64), ("path", ctypes.c_int32 * 65),
                 ("mask", ctypes.c_uint8 * 128), ("dp_value", ctypes.c_float), ("ema", ctypes.c_double * 3)]
+
+
+class KV8CacheC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("pool_pages", ctypes.c_int), ("layer", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("block_tokens", ctypes.c_int)]
+
+
+class KV8RowsC(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("ld_k", ctypes.c_int64), ("ld_v", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("first", ctypes.c_int), ("rows", ctypes.c_int)]
+
+
+class KV8AttentionArgsC(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("ld_q", ctypes.c_int64),
+                ("ld_out", ctypes.c_int64), ("dtype", ctypes.c_int), ("n_q_heads", ctypes.c_int),
+                ("rows", ctypes.c_int), ("prefix", ctypes.c_int), ("base", ctypes.c_int), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float), ("mask", ctypes.c_uint64 * 64)]
+
+
+class KV8EvictArgsC(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("ld_weight", ctypes.c_int64), ("index", ctypes.c_void_p),
+                ("kept_weight", ctypes.c_void_p), ("n", ctypes.c_int), ("keep", ctypes.c_int),
+                ("recent", ctypes.c_int)]
 
 
 _libs = {}
@@ -137,6 +163,12 @@ def load_library(xcheck: bool = False) -> ctypes.CDLL:
                                      ctypes.POINTER(ctypes.c_int)]),
         "ssd_gemv_warps": (ctypes.c_int64, [I, ctypes.c_int64]),
         "ssd_attn_ring_rule": (None, [I, I, I, ctypes.POINTER(I), ctypes.POINTER(I)]),
+        "ssd_kv8_append": (I, [P, P, P]),
+        "ssd_kv8_read": (I, [P, P, P]),
+        "ssd_kv8_attention_scratch_bytes": (ctypes.c_size_t, [P, P]),
+        "ssd_kv8_attention": (I, [P, P, P, ctypes.c_size_t, P]),
+        "ssd_kv8_weights": (I, [P, P, ctypes.c_uint64, P, P, ctypes.c_int64, P]),
+        "ssd_kv8_evict": (I, [P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -513,3 +545,6 @@ class Engine:
         n = (ctypes.c_int64 * 4)()
         self._check(self.lib.ssd_get_pass_times(self.ctx, ms, n))
         return {k: (ms[i], n[i]) for i, k in enumerate(("draft", "verify", "dp", "ar"))}
+
+
+from .kv8 import KVCache8  # noqa: E402,F401  (uses the names above)

@@ -1519,9 +1519,10 @@ ssd_status ssd_set_ema(ssd_ctx* ctx, const double* ema, int n_levels) {
 int ssd_cascade_depth(int n_layers, int n_levels, int seq_len) { return cascade_depth(n_layers, n_levels, seq_len); }
 
 void ssd_abi_sizes(size_t* out, int n) {
-  const size_t sz[5] = {sizeof(ssd_model_config), sizeof(ssd_policy), sizeof(ssd_stats), sizeof(ssd_attention_args),
-                        sizeof(ssd_cycle_record)};
-  for (int i = 0; i < n && i < 5; ++i) out[i] = sz[i];
+  const size_t sz[9] = {sizeof(ssd_model_config), sizeof(ssd_policy), sizeof(ssd_stats), sizeof(ssd_attention_args),
+                        sizeof(ssd_cycle_record), sizeof(ssd_kv8_cache), sizeof(ssd_kv8_rows),
+                        sizeof(ssd_kv8_attention_args), sizeof(ssd_kv8_evict_args)};
+  for (int i = 0; i < n && i < 9; ++i) out[i] = sz[i];
 }
 
 namespace {

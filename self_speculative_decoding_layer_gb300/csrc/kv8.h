@@ -1,0 +1,58 @@
+// Host-side launch interface of the 8-bit KV cache's kernels (internal; not part of the C ABI).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kv8.cuh"
+
+namespace ssd {
+
+// Rows to append to a cache (k, v are read) or values to read from it (k, v are written), 16-byte aligned.
+struct Kv8RowsArgs {
+  void* k;
+  void* v;
+  size_t ld_k, ld_v;  // elements between rows
+  int first, rows;    // slots first .. first + rows - 1
+};
+
+struct Kv8SelectArgs {
+  const float* weight;  // [n_kv][ld_weight]
+  size_t ld_weight;
+  int n, keep, recent;
+  int* index;           // [n_kv][keep]
+  float* kept_weight;   // [n_kv][keep] or null
+};
+
+struct Kv8AttnArgs {
+  Kv8View c;
+  const void* q;    // [rows][ld_q], query heads of hd
+  void* out;        // [rows][ld_out]
+  float* lse;       // [rows][n_q] or null; the weights kernel reads it
+  size_t ld_q, ld_out;
+  int n_q, group, rows;
+  int prefix, base;
+  float scale, cap;          // cap 0: none
+  unsigned long long any;    // union of the masks
+  int n_split;               // key splits; more than one: partial results, merged by a second kernel
+  float* part_o;             // [n_kv * queries][n_split][hd]
+  float2* part_ml;           // [n_kv * queries][n_split]: running maximum (log2) and sum
+  // weights kernel
+  const float* w_in;         // [n_kv][ld_w] or null
+  float* w_out;
+  size_t ld_w;
+  int n_take;                // query rows that count
+  unsigned char take[kMaxRows];
+  unsigned long long mask[kMaxRows];
+};
+
+// io: ssd_dtype of q / out, k / v rows.
+bool launch_kv8_append(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st);
+bool launch_kv8_read(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st);
+bool launch_kv8_evict(const Kv8View& src, const Kv8View& dst, const Kv8SelectArgs& a, cudaStream_t st);
+// Key splits of an attention launch over `slots` slots.
+int kv8_attention_splits(int rows, int group, int n_kv, int slots);
+bool launch_kv8_attention(const Kv8AttnArgs& a, int io, cudaStream_t st);
+bool launch_kv8_weights(const Kv8AttnArgs& a, int io, cudaStream_t st);
+
+}  // namespace ssd
