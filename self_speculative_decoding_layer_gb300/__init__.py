@@ -547,4 +547,11 @@ class Engine:
         return {k: (ms[i], n[i]) for i, k in enumerate(("draft", "verify", "dp", "ar"))}
 
 
-from .kv8 import KVCache8  # noqa: E402,F401  (uses the names above)
+def __getattr__(name: str):
+    # the 8-bit cache's module imports torch, which the rest of this module does only where it is used
+    if name == "KVCache8":
+        from .kv8 import KVCache8
+
+        globals()[name] = KVCache8
+        return KVCache8
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -20,6 +20,7 @@
 // k_kv8_weights recomputes the scores and adds exp(s - lse) over the chosen
 // rows and the KV head's queries to an accumulator: each sixteen-slot tile is
 // one warp's, so nothing is shared and the sums have one order.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "kv8.h"
@@ -28,7 +29,9 @@ namespace ssd {
 
 namespace {
 
-constexpr int kAttnWarps = 8;
+constexpr int kTileSlots = 32;   // slots that a warp takes at a time, all in one page
+constexpr int kMaxCluster = 8;   // key splits that merge in distributed shared memory
+constexpr int kMaxSplits = 152;  // key splits that merge through global memory
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 14.f;  // softmax weights are held times 2^14, within fp16's normal range
 
@@ -47,20 +50,32 @@ __device__ __forceinline__ uint32_t pack_rest2(float a, float b, uint32_t hi) {
   return pack_half2(a - f.x, b - f.y);
 }
 
-// Tiles of sixteen slots: those of the prefix, then those that hold new slots past them.
+// Tiles of 2^SHIFT slots: those of the prefix, then those that hold new slots past them.
+template <int SHIFT>
 struct Tiles {
   int n_prefix, first_new, n;
-  __device__ __forceinline__ Tiles(int prefix, int base, int rows) {
-    n_prefix = (prefix + 15) >> 4;
-    first_new = max(n_prefix, base >> 4);
-    n = n_prefix + max(0, ((base + rows + 15) >> 4) - first_new);
+  __host__ __device__ __forceinline__ Tiles(int prefix, int base, int rows) {
+    constexpr int up = (1 << SHIFT) - 1;
+    n_prefix = (prefix + up) >> SHIFT;
+    first_new = base >> SHIFT;
+    if (first_new < n_prefix) first_new = n_prefix;
+    const int end = (base + rows + up) >> SHIFT;
+    n = n_prefix + (end > first_new ? end - first_new : 0);
   }
-  __device__ __forceinline__ int slot(int t) const { return (t < n_prefix ? t : first_new + t - n_prefix) << 4; }
+  __device__ __forceinline__ int slot(int t) const { return (t < n_prefix ? t : first_new + t - n_prefix) << SHIFT; }
 };
 
 __device__ __forceinline__ bool visible(int slot, int prefix, int base, unsigned long long mask) {
   const unsigned e = (unsigned)(slot - base);
   return slot < prefix || (e < 64u && ((mask >> e) & 1ull));
+}
+
+// Whether any row sees one of the sixteen slots from `slot` on.
+__device__ __forceinline__ bool visible_any(int slot, const Kv8AttnArgs& a) {
+  if (slot < a.prefix) return true;
+  const int e = slot - a.base;
+  if (e <= -16 || e >= 64) return false;
+  return ((e >= 0 ? a.any >> e : a.any << -e) & 0xffffull) != 0;
 }
 
 __device__ __forceinline__ uint4 ld16(const uint8_t* p) {
@@ -118,11 +133,12 @@ __device__ __forceinline__ float stage_query(const T* q, uint32_t* hi, uint32_t*
 
 __device__ __forceinline__ uint32_t word_of(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
 
-// S^T += K Q^T for a tile of sixteen keys (klo: rows g, khi: rows g + 8) and QT query columns of eight.
-template <int HD, int CODE, bool SPLIT, int QT>
+// S^T += K Q^T for sixteen keys (klo: rows g, khi: rows g + 8) and eight queries per QT; query(t, i) is the fp16
+// pair of word i of operand t that this lane multiplies (hi words, then lo words).
+template <int HD, int CODE, bool SPLIT, int QT, typename Query>
 __device__ __forceinline__ void scores(float (&s)[QT][4], const uint4 (&klo)[HD / 64], const uint4 (&khi)[HD / 64],
-                                       const uint32_t* qhi, const uint32_t* qlo, int lane) {
-  constexpr int QW = HD / 16 * 64;  // words of one eight-query operand
+                                       const Query& query) {
+  constexpr int STEPS = HD / 16;
 #pragma unroll
   for (int j = 0; j < HD / 64; ++j) {
 #pragma unroll
@@ -130,39 +146,150 @@ __device__ __forceinline__ void scores(float (&s)[QT][4], const uint4 (&klo)[HD 
       uint32_t a[4];
       codes_to_half<CODE>(word_of(klo[j], i), a[0], a[2]);
       codes_to_half<CODE>(word_of(khi[j], i), a[1], a[3]);
-      const int at = (4 * j + i) * 64 + lane;
+      const int step = 4 * j + i;
 #pragma unroll
       for (int t = 0; t < QT; ++t) {
-        mma16816(s[t], a, qhi[t * QW + at], qhi[t * QW + at + 32]);
-        if (SPLIT) mma16816(s[t], a, qlo[t * QW + at], qlo[t * QW + at + 32]);
+        mma16816(s[t], a, query(t, 2 * step), query(t, 2 * step + 1));
+        if (SPLIT) mma16816(s[t], a, query(t, 2 * (STEPS + step)), query(t, 2 * (STEPS + step) + 1));
       }
     }
   }
 }
 
-// Score in the log2 domain of product x with coefficient c (scale * inverse scales [* log2 e without a cap]).
-__device__ __forceinline__ float capped(float x, float c, float cap) { return cap * tanhf(x * c / cap) * kLog2e; }
+// The capped score in the log2 domain: tanh y = 1 - 2 / (1 + e^2y), whose error of a few 2^-24 is absolute, so that
+// a score is off by that many parts of the cap.
+__device__ __forceinline__ float capped(float x, float cap) {
+  const float e = exp2_approx(x * (2.f * kLog2e / cap));
+  return cap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
+}
 
-// Grid (splits, KV heads, query blocks of 8 QT).
+// A warp's ring of 32-slot tiles in shared memory: the K rows, then the V rows.  Sixteen-byte chunks are swizzled
+// inside 128-byte lines, so that neither a lane's chunks of its own K row nor its run of four V rows meet in a bank.
+template <int HD, int STAGES>
+struct Ring {
+  static constexpr int kStages = STAGES;
+  static constexpr int kTensor = kTileSlots * HD;  // bytes of K (or V) of one tile
+  static constexpr int kStage = 2 * kTensor;
+  static constexpr int kWarp = kStages * kStage;
+  static __device__ __forceinline__ int at(int row, int byte) {
+    if (HD == 128) return row * 128 + (byte ^ ((row & 7) << 4));
+    return (row >> 1) * 128 + ((((row & 1) << 6) | byte) ^ (((row >> 1) & 3) << 5));
+  }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Four neighbouring values of an output row.
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float4& y) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = y;
+  } else {
+    __align__(8) T t[4] = {Io<T>::from_f(y.x), Io<T>::from_f(y.y), Io<T>::from_f(y.z), Io<T>::from_f(y.w)};
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(t);
+  }
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2; }
+
+// Warps of a CTA and stages of a warp's ring.  Eight queries leave registers for twelve warps, which hide the
+// latency of the conversions, with two stages each (8 KB under way a warp, 96 KB an SM); the larger blocks run
+// eight warps with three.
+template <int HD, int QT>
+struct AttnShape {
+  static constexpr int W = QT == 1 ? 12 : 8;
+  using R = Ring<HD, QT == 1 ? 2 : 3>;
+};
+
+template <typename T, int HD, int QT>
+struct AttnSmem {
+  using R = typename AttnShape<HD, QT>::R;
+  static constexpr int W = AttnShape<HD, QT>::W;
+  static constexpr int QB = 8 * QT;
+  static constexpr int QW = HD / 16 * 64;                                   // words of one eight-query operand
+  static constexpr int kQ = QT * QW * 4 * (sizeof(T) == 4 ? 2 : 1);         // staged queries
+  static constexpr int kRing = W * R::kWarp;
+  static constexpr int OS = HD + 4;                                         // row stride of the merge buffers
+  static constexpr int kMerge = W * QB * OS * 4;                            // over the ring, after the loop
+  static constexpr int kHead = W * R::kStages * 32;                         // tile headers (TileHead)
+  static constexpr int kBytes = kQ + (kRing > kMerge ? kRing : kMerge) + kHead;
+};
+
+struct __align__(16) TileHead {
+  float ks[2], vs[2];  // scales of the tile's halves
+  int used, pad[3];    // whether the tile's page is one
+};
+
+// Grid (splits, KV heads, query blocks of 8 QT).  With part_o the splits' results go to scratch; else, when there
+// is more than one, the splits of a query block are one cluster.
 template <typename T, int HD, int CODE, int QT>
-__global__ void __launch_bounds__(kAttnWarps * 32, 2) k_kv8_attention(const __grid_constant__ Kv8AttnArgs a) {
+__global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(const __grid_constant__ Kv8AttnArgs a) {
+  namespace cg = cooperative_groups;
+  using L = AttnSmem<T, HD, QT>;
+  using R = typename L::R;
+  constexpr int W = L::W;
   constexpr bool SPLIT = sizeof(T) == 4;
-  constexpr int NJ = HD / 64;        // sixteen-byte chunks of a row per lane
-  constexpr int QB = 8 * QT;
-  constexpr int QW = HD / 16 * 64;   // words of one eight-query operand
+  constexpr int NJ = HD / 64;        // sixteen-byte chunks of a K row per lane
+  constexpr int QB = L::QB, QW = L::QW, OS = L::OS;
   constexpr int DT = HD / 16;        // head-dim tiles of O^T
-  constexpr int OS = QB + 1;         // row stride of the merge buffer
-  extern __shared__ uint32_t smem[];
-  uint32_t* s_hi = smem;                       // [QT][QW]
-  uint32_t* s_lo = smem + QT * QW;             // [QT][QW] when SPLIT
-  float* s_o = reinterpret_cast<float*>(smem); // after the loop: [warps][HD][OS]
+  extern __shared__ __align__(128) unsigned char s_dyn[];
+  uint32_t* s_hi = reinterpret_cast<uint32_t*>(s_dyn);   // [QT][QW]
+  uint32_t* s_lo = s_hi + QT * QW;                       // [QT][QW] when SPLIT
+  float* s_o = reinterpret_cast<float*>(s_dyn + L::kQ);  // after the loop: [warps][QB][OS]
   __shared__ float s_inv[QB];
-  __shared__ float s_m[kAttnWarps][QB], s_l[kAttnWarps][QB];
+  __shared__ float s_m[W][QB], s_l[W][QB];
+  __shared__ float2 s_ml[QB];        // this CTA's maximum and sum
+  __shared__ float2 s_f[kMaxCluster][QB];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int split = blockIdx.x, h = blockIdx.y, q0 = blockIdx.z * QB;
   const int nq = a.rows * a.group;
   griddep_launch();
-  for (int q = warp; q < QB; q += kAttnWarps) {
+
+  const Tiles<5> tiles(a.prefix, a.base, a.rows);
+  const int t_first = split * a.split_tiles, t_last = min(tiles.n, t_first + a.split_tiles);
+  const unsigned char* ring = s_dyn + L::kQ + warp * R::kWarp;
+  TileHead* heads = reinterpret_cast<TileHead*>(s_dyn + L::kBytes - L::kHead) + warp * R::kStages;
+
+  // Tile ti (physical page `page`) into ring stage st; one group of copies whether or not there is a tile.
+  auto fill = [&](int st, int ti, int page) {
+    const bool ok = ti < t_last && a.c.page_ok(page);
+    if (ok) {
+      const int in_page = tiles.slot(ti) % kPage;
+      const size_t row0 = a.c.page_row(page, h) + (size_t)in_page * HD + lane * 16;
+      const uint32_t dst = smem_u32(ring + st * R::kStage);
+#pragma unroll
+      for (int i = 0; i < HD / 16; ++i) {
+        const int x = (i * 32 + lane) * 16, to = R::at(x / HD, x % HD);
+        cp_async16(dst + to, a.c.k + row0 + i * 512);
+        cp_async16(dst + R::kTensor + to, a.c.v + row0 + i * 512);
+      }
+      if (lane < 4)
+        cp_async4(smem_u32(&heads[st]) + lane * 4,
+                  (lane & 2 ? a.c.vs : a.c.ks) + a.c.scale_at(page, h, in_page + (lane & 1) * 16));
+    }
+    if (lane == 4) heads[st].used = ok;
+    cp_async_commit();
+  };
+  auto page_of = [&](int ti) { return ti < t_last ? __ldg(a.c.btab + tiles.slot(ti) / kPage) : -1; };
+
+  int pages[R::kStages];
+#pragma unroll
+  for (int i = 0; i < R::kStages; ++i) pages[i] = page_of(t_first + warp + i * W);
+#pragma unroll
+  for (int i = 0; i < R::kStages - 1; ++i) fill(i, t_first + warp + i * W, pages[i]);
+  int page_next = pages[R::kStages - 1];
+
+  for (int q = warp; q < QB; q += W) {
     const int qi = q0 + q;
     const T* p = nullptr;
     if (qi < nq) {
@@ -174,22 +301,15 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) k_kv8_attention(const __gr
   }
   __syncthreads();
 
-  const Tiles tiles(a.prefix, a.base, a.rows);
-  const int t_first = (int)((long long)tiles.n * split / a.n_split);
-  const int t_last = (int)((long long)tiles.n * (split + 1) / a.n_split);
   const bool cap = a.cap > 0.f;
-
   float coef[QT][2];
-  unsigned long long mask[QT][2];
   float m[QT][2], l[QT][2], o[QT][DT][4];
-  float vref = 0.f;  // O^T is held in units of this scale of V
+  float vref = 0.f, vinv = 0.f;  // O^T is held in units of vref, a scale of V
 #pragma unroll
   for (int t = 0; t < QT; ++t)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int q = t * 8 + 2 * c + e;
-      coef[t][e] = a.scale * s_inv[q] * (cap ? 1.f : kLog2e);
-      mask[t][e] = q0 + q < nq ? a.mask[(q0 + q) / a.group] : 0ull;
+      coef[t][e] = a.scale * s_inv[t * 8 + 2 * c + e] * (cap ? 1.f : kLog2e);
       m[t][e] = -INFINITY;
       l[t][e] = 0.f;
     }
@@ -200,120 +320,187 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) k_kv8_attention(const __gr
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][d][e] = 0.f;
 
-  for (int ti = t_first + warp; ti < t_last; ti += kAttnWarps) {
+  // The staged queries: in registers for eight of them, else read again for every tile.
+  constexpr int QWORDS = HD / 8 * (SPLIT ? 2 : 1);
+  uint32_t qreg[QT == 1 ? QWORDS : 1];
+  if constexpr (QT == 1) {
+#pragma unroll
+    for (int i = 0; i < QWORDS; ++i) qreg[i] = s_hi[i * 32 + lane];
+  }
+  auto query = [&](int t, int i) -> uint32_t {
+    if constexpr (QT == 1) return qreg[i];
+    return i < HD / 8 ? s_hi[t * QW + i * 32 + lane] : s_lo[t * QW + (i - HD / 8) * 32 + lane];
+  };
+
+  int st = 0;
+  for (int ti = t_first + warp; ti < t_last; ti += W) {
+    cp_async_wait<R::kStages - 2>();
+    __syncwarp();  // every lane's copies of this stage have landed; the stage before it is free
+    {
+      const int ahead = ti + (R::kStages - 1) * W;
+      fill(st == 0 ? R::kStages - 1 : st - 1, ahead, page_next);
+      page_next = page_of(ahead + W);
+    }
+    const unsigned char* kbuf = ring + st * R::kStage;
+    const unsigned char* vbuf = kbuf + R::kTensor;
+    const TileHead head = heads[st];
+    st = st + 1 == R::kStages ? 0 : st + 1;
+    if (!head.used) continue;
     const int slot0 = tiles.slot(ti);
-    const int page = a.c.btab[slot0 / kPage];
-    if (!a.c.page_ok(page)) continue;
-    const size_t row0 = a.c.page_row(page, h) + (size_t)(slot0 % kPage) * HD;
-    uint4 klo[NJ], khi[NJ], v[4][HD / 128 ? 1 : 1];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      klo[j] = ld16(a.c.k + row0 + (size_t)g * HD + (c + 4 * j) * 16);
-      khi[j] = ld16(a.c.k + row0 + (size_t)(g + 8) * HD + (c + 4 * j) * 16);
-    }
-    // V: keys 2c, 2c + 1, 2c + 8, 2c + 9; head dims g * HD / 8 ..
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint8_t* p = a.c.v + row0 + (size_t)(2 * c + (e & 1) + (e >> 1) * 8) * HD + g * (HD / 8);
-      if (HD == 128) {
-        v[e][0] = ld16(p);
-      } else {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-        v[e][0] = make_uint4(u.x, u.y, 0u, 0u);
-      }
-    }
-    const size_t sc = a.c.scale_at(page, h, slot0 % kPage);
-    const float ks = __ldg(a.c.ks + sc);
-    float vs = __ldg(a.c.vs + sc);
 
-    float s[QT][4];
+    uint4 klo[2][NJ], khi[2][NJ];
 #pragma unroll
-    for (int t = 0; t < QT; ++t)
+    for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-    scores<HD, CODE, SPLIT, QT>(s, klo, khi, s_hi, s_lo, lane);
-
-    const bool full = slot0 + 16 <= a.prefix;
-#pragma unroll
-    for (int t = 0; t < QT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float cf = coef[t][e & 1] * ks;
-        s[t][e] = cap ? capped(s[t][e], cf, a.cap) : s[t][e] * cf;
-        if (!full && !visible(slot0 + g + (e >> 1) * 8, a.prefix, a.base, mask[t][e & 1])) s[t][e] = -INFINITY;
+      for (int j = 0; j < NJ; ++j) {
+        klo[b][j] = *reinterpret_cast<const uint4*>(kbuf + R::at(b * 16 + g, (c + 4 * j) * 16));
+        khi[b][j] = *reinterpret_cast<const uint4*>(kbuf + R::at(b * 16 + g + 8, (c + 4 * j) * 16));
       }
-    if (!full) {  // rows that hold no token may hold any bits
+    float s[2][QT][4];  // halves of sixteen keys
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (!visible(slot0 + 2 * c + (e & 1) + (e >> 1) * 8, a.prefix, a.base, a.any)) v[e][0] = make_uint4(0u, 0u, 0u, 0u);
-    }
-
-    // running maximum of each query column
-    float alpha[QT][2];
-    bool grow = vs > vref;
-#pragma unroll
-    for (int t = 0; t < QT; ++t)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(s[t][e], s[t][e + 2]);
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        const float mn = fmaxf(m[t][e], x);
-        alpha[t][e] = mn > m[t][e] ? exp2_approx(m[t][e] - mn) : 1.f;  // (m = -inf: 0)
-        grow |= mn > m[t][e];
-        m[t][e] = mn;
-        l[t][e] *= alpha[t][e];
-      }
-    if (__any_sync(0xffffffffu, grow)) {
-      float av = 1.f;
-      if (vs > vref) {
-        av = vref / vs;
-        vref = vs;
-      }
+    for (int b = 0; b < 2; ++b) {
 #pragma unroll
       for (int t = 0; t < QT; ++t)
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[t][d][e] *= alpha[t][e & 1] * av;
+        for (int e = 0; e < 4; ++e) s[b][t][e] = 0.f;
+      scores<HD, CODE, SPLIT, QT>(s[b], klo[b], khi[b], query);
     }
-    const float rv = vref > 0.f ? vs / vref : 0.f;  // at most 1
 
-    uint32_t ph[QT][2], pl[QT][2];
+    const bool full = slot0 + kTileSlots <= a.prefix;
+    float vmax = fmaxf(head.vs[0], head.vs[1]);
 #pragma unroll
     for (int t = 0; t < QT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {  // keys g (e = 0) and g + 8
-        float p[2];
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) s[b][t][2 * r + u] *= coef[t][u] * head.ks[b];
+    if (cap) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[b][t][e] = capped(s[b][t][e], a.cap);
+    }
+    if (!full) {
+      vmax = fmaxf(visible_any(slot0, a) ? head.vs[0] : 0.f, visible_any(slot0 + 16, a) ? head.vs[1] : 0.f);
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float mm = m[t][u] == -INFINITY ? 0.f : m[t][u];
-          const float x = exp2_approx(s[t][2 * e + u] - mm + kPShift);
-          l[t][u] += x;
-          p[u] = x * rv;
+          const int qi = q0 + t * 8 + 2 * c + u;
+          const unsigned long long mask = qi < nq ? a.mask[qi / a.group] : 0ull;
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (!visible(slot0 + b * 16 + r * 8 + g, a.prefix, a.base, mask)) s[b][t][2 * r + u] = -INFINITY;
         }
-        const uint32_t hi = pack_half2(p[0], p[1]);
-        ph[t][e] = transpose8x8(hi);
-        if (SPLIT) pl[t][e] = transpose8x8(pack_rest2(p[0], p[1], hi));
+    }
+
+    // running maximum of each query column
+    bool grow = vmax > vref;
+    float top[QT][2];
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float x = fmaxf(fmaxf(s[0][t][u], s[0][t][u + 2]), fmaxf(s[1][t][u], s[1][t][u + 2]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        top[t][u] = x;
+        grow |= x > m[t][u];
       }
-    // O^T += V^T P^T: head-dim tile d holds dims 2d and 2d + 1 of every lane's run
+    if (__any_sync(0xffffffffu, grow)) {
+      float av = 1.f;
+      if (vmax > vref) {
+        av = vref / vmax;
+        vref = vmax;
+        vinv = 1.f / vmax;
+      }
 #pragma unroll
-    for (int w = 0; w < DT / 2; ++w) {
-      uint32_t x0[4], x1[4];
-      pair_to_half<CODE>(word_of(v[0][0], w), word_of(v[1][0], w), x0);
-      pair_to_half<CODE>(word_of(v[2][0], w), word_of(v[3][0], w), x1);
+      for (int t = 0; t < QT; ++t) {
+        float alpha[2];
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const uint32_t fa[4] = {x0[2 * d], x0[2 * d + 1], x1[2 * d], x1[2 * d + 1]};
+        for (int u = 0; u < 2; ++u) {
+          const float mn = fmaxf(m[t][u], top[t][u]);
+          alpha[u] = mn > m[t][u] ? exp2_approx(m[t][u] - mn) : 1.f;  // (m = -inf: 0)
+          m[t][u] = mn;
+          l[t][u] *= alpha[u];
+          alpha[u] *= av;
+        }
 #pragma unroll
-        for (int t = 0; t < QT; ++t) {
-          mma16816(o[t][2 * w + d], fa, ph[t][0], ph[t][1]);
-          if (SPLIT) mma16816(o[t][2 * w + d], fa, pl[t][0], pl[t][1]);
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[t][d][e] *= alpha[e & 1];
+      }
+    }
+    float shift[QT][2];  // what is left of a score before the exponential
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) shift[t][u] = kPShift - (m[t][u] == -INFINITY ? 0.f : m[t][u]);
+
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      // at most 1 where the half has a visible slot (elsewhere the scale may be anything, and no weight is used)
+      const float rv = head.vs[b] <= vref ? head.vs[b] * vinv : 0.f;
+      uint32_t ph[QT][2], pl[QT][2];
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // keys g and g + 8
+          float p[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float x = exp2_approx(s[b][t][2 * r + u] + shift[t][u]);
+            l[t][u] += x;
+            p[u] = x * rv;
+          }
+          const uint32_t hi = pack_half2(p[0], p[1]);
+          ph[t][r] = transpose8x8(hi);
+          if (SPLIT) pl[t][r] = transpose8x8(pack_rest2(p[0], p[1], hi));
+        }
+      // V: keys 2c, 2c + 1, 2c + 8, 2c + 9 of the half; head dims g * HD / 8 ..
+      uint4 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = b * 16 + 2 * c + (e & 1) + (e >> 1) * 8;
+        if (HD == 128) {
+          v[e] = *reinterpret_cast<const uint4*>(vbuf + R::at(row, g * 16));
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(vbuf + R::at(row, g * 8));
+          v[e] = make_uint4(w.x, w.y, 0u, 0u);
+        }
+      }
+      if (!full) {  // rows that hold no token may hold any bits
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!visible(slot0 + b * 16 + 2 * c + (e & 1) + (e >> 1) * 8, a.prefix, a.base, a.any))
+            v[e] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      // O^T += V^T P^T: head-dim tile d holds dims 2d and 2d + 1 of every lane's run
+#pragma unroll
+      for (int w = 0; w < DT / 2; ++w) {
+        uint32_t x0[4], x1[4];
+        pair_to_half<CODE>(word_of(v[0], w), word_of(v[1], w), x0);
+        pair_to_half<CODE>(word_of(v[2], w), word_of(v[3], w), x1);
+#pragma unroll
+        for (int d = 0; d < 2; ++d) {
+          const uint32_t fa[4] = {x0[2 * d], x0[2 * d + 1], x1[2 * d], x1[2 * d + 1]};
+#pragma unroll
+          for (int t = 0; t < QT; ++t) {
+            mma16816(o[t][2 * w + d], fa, ph[t][0], ph[t][1]);
+            if (SPLIT) mma16816(o[t][2 * w + d], fa, pl[t][0], pl[t][1]);
+          }
         }
       }
     }
   }
+  cp_async_wait<0>();
 
   // Merge the warps: sums over the lanes of a column, then over the warps in order.
 #pragma unroll
@@ -329,130 +516,213 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 2) k_kv8_attention(const __gr
         s_l[warp][t * 8 + 2 * c + e] = x;
       }
     }
-  __syncthreads();  // the staged queries are not read any more
+  __syncthreads();  // no warp reads its ring any more
 #pragma unroll
   for (int t = 0; t < QT; ++t)
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int dim = g * (HD / 8) + 2 * d + (e >> 1);
-        s_o[(warp * HD + dim) * OS + t * 8 + 2 * c + (e & 1)] = o[t][d][e] * vref;
-      }
+      for (int d = 0; d < DT; d += 2)
+        *reinterpret_cast<float4*>(s_o + (size_t)(warp * QB + t * 8 + 2 * c + e) * OS + g * (HD / 8) + 2 * d) =
+            make_float4(o[t][d][e] * vref, o[t][d][e + 2] * vref, o[t][d + 1][e] * vref, o[t][d + 1][e + 2] * vref);
   __syncthreads();
-  for (int i = threadIdx.x; i < QB * HD; i += kAttnWarps * 32) {
-    const int q = i / HD, d = i - q * HD, qi = q0 + q;
-    if (qi >= nq) break;
+  constexpr int ITEMS = QB * HD / 4;  // four dims of a query
+  constexpr int PER = (ITEMS + W * 32 - 1) / (W * 32);
+  float4 mine[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = threadIdx.x + j * W * 32;
+    if (i >= ITEMS) break;
+    const int q = i / (HD / 4), d = (i % (HD / 4)) * 4;
     float M = s_m[0][q];
 #pragma unroll
-    for (int w = 1; w < kAttnWarps; ++w) M = fmaxf(M, s_m[w][q]);
+    for (int w = 1; w < W; ++w) M = fmaxf(M, s_m[w][q]);
     const float ref = M == -INFINITY ? 0.f : M;
-    float x = 0.f, L = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float f = exp2_approx(s_m[w][q] - ref);
-      x += s_o[(w * HD + d) * OS + q] * f;
-      L += s_l[w][q] * f;
+      const float4 y = *reinterpret_cast<const float4*>(s_o + (size_t)(w * QB + q) * OS + d);
+      x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
+      sum += s_l[w][q] * f;
     }
-    if (a.n_split > 1) {
+    mine[j] = x;
+    if (d == 0) s_ml[q] = make_float2(M, sum);
+  }
+
+  auto output = [&](int q, int d, const float4& x, float M, float sum) {
+    const int qi = q0 + q;
+    if (qi >= nq) return;
+    const int r = qi / a.group, head = h * a.group + qi - r * a.group;
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
+    store4(reinterpret_cast<T*>(a.out) + (size_t)r * a.ld_out + (size_t)head * HD + d,
+           make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
+    if (d == 0 && a.lse) a.lse[(size_t)r * a.n_q + head] = lse_of(M, sum);
+  };
+
+  __syncthreads();
+  if (a.part_o) {  // partial results, merged by k_kv8_merge
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = threadIdx.x + j * W * 32;
+      if (i >= ITEMS) break;
+      const int q = i / (HD / 4), d = (i % (HD / 4)) * 4, qi = q0 + q;
+      if (qi >= nq) break;
       const size_t at = ((size_t)h * nq + qi) * a.n_split + split;
-      a.part_o[at * HD + d] = x;
-      if (d == 0) a.part_ml[at] = make_float2(M, L);
-    } else {
-      const int r = qi / a.group, head = h * a.group + qi - r * a.group;
-      const float y = L == 0.f ? 0.f : x / L;
-      T* out = reinterpret_cast<T*>(a.out) + (size_t)r * a.ld_out + (size_t)head * HD + d;
-      if constexpr (SPLIT)
-        *out = y;
-      else
-        *out = Io<T>::from_f(y);
-      if (d == 0 && a.lse) a.lse[(size_t)r * a.n_q + head] = L == 0.f ? -INFINITY : (M - kPShift + log2f(L)) * kLn2;
+      *reinterpret_cast<float4*>(a.part_o + at * HD + d) = mine[j];
+      if (d == 0) a.part_ml[at] = s_ml[q];
     }
+  } else if (a.n_split == 1) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = threadIdx.x + j * W * 32;
+      if (i >= ITEMS) break;
+      const int q = i / (HD / 4), d = (i % (HD / 4)) * 4;
+      output(q, d, mine[j], s_ml[q].x, s_ml[q].y);
+    }
+  } else {  // the cluster's partial results lie in its CTAs' shared memory; rank r adds every n_split-th item
+    cg::cluster_group cl = cg::this_cluster();
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = threadIdx.x + j * W * 32;
+      if (i < ITEMS) *reinterpret_cast<float4*>(s_o + i * 4) = mine[j];
+    }
+    cl.sync();
+    for (int i = threadIdx.x; i < QB * a.n_split; i += W * 32) s_f[i / QB][i % QB] = cl.map_shared_rank(s_ml, i / QB)[i % QB];
+    __syncthreads();
+    for (int i = split + threadIdx.x * a.n_split; i < ITEMS; i += W * 32 * a.n_split) {
+      const int q = i / (HD / 4), d = (i % (HD / 4)) * 4;
+      float4 y[kMaxCluster];
+      float M = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < a.n_split) {
+          y[r] = *reinterpret_cast<const float4*>(cl.map_shared_rank(s_o, r) + i * 4);
+          M = fmaxf(M, s_f[r][q].x);
+        }
+      const float ref = M == -INFINITY ? 0.f : M;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < a.n_split) {
+          const float f = exp2_approx(s_f[r][q].x - ref);
+          x.x += y[r].x * f, x.y += y[r].y * f, x.z += y[r].z * f, x.w += y[r].w * f;
+          sum += s_f[r][q].y * f;
+        }
+      output(q, d, x, M, sum);
+    }
+    cl.sync();  // no CTA leaves while another may read its shared memory
   }
 }
 
-// Grid (queries / 4): one warp for each query adds its splits in order.
+// Grid (queries of all heads): thread t adds dim t of its query over the splits, in order.
 template <typename T, int HD>
-__global__ void __launch_bounds__(128) k_kv8_merge(const __grid_constant__ Kv8AttnArgs a) {
-  constexpr int DPL = HD / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(HD) k_kv8_merge(const __grid_constant__ Kv8AttnArgs a) {
+  __shared__ float2 s_f[kMaxSplits];
+  __shared__ float red[HD / 32];
   const int nq = a.rows * a.group;
-  const int i = blockIdx.x * 4 + warp;
-  griddep_wait();
-  if (i >= a.c.n_kv * nq) return;
+  const int i = blockIdx.x;
   const int h = i / nq, qi = i - h * nq, r = qi / a.group, head = h * a.group + qi - r * a.group;
+  griddep_wait();
   const float2* ml = a.part_ml + (size_t)i * a.n_split;
+  const float* po = a.part_o + (size_t)i * a.n_split * HD + threadIdx.x;
+  float first[8];
+#pragma unroll
+  for (int s = 0; s < 8; ++s) first[s] = s < a.n_split ? po[(size_t)s * HD] : 0.f;
   float M = -INFINITY;
-  for (int s = lane; s < a.n_split; s += 32) M = fmaxf(M, ml[s].x);
-  M = warp_max(M);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f, x[DPL];
-#pragma unroll
-  for (int d = 0; d < DPL; ++d) x[d] = 0.f;
-  const float* po = a.part_o + (size_t)i * a.n_split * HD + lane * DPL;
-#pragma unroll 8
-  for (int s = 0; s < a.n_split; ++s) {
+  for (int s = threadIdx.x; s < a.n_split; s += HD) {
     const float2 t = ml[s];
+    s_f[s] = t;
+    M = fmaxf(M, t.x);
+  }
+  M = warp_max(M);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < HD / 32; ++w) M = fmaxf(M, red[w]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float sum = 0.f, x = 0.f;
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    if (s < a.n_split) {
+      const float2 t = s_f[s];
+      const float f = exp2_approx(t.x - ref);
+      sum += t.y * f;
+      x += first[s] * f;
+    }
+#pragma unroll 8
+  for (int s = 8; s < a.n_split; ++s) {
+    const float2 t = s_f[s];
     const float f = exp2_approx(t.x - ref);
-    L += t.y * f;
-#pragma unroll
-    for (int d = 0; d < DPL; ++d) x[d] += po[(size_t)s * HD + d] * f;
+    sum += t.y * f;
+    x += po[(size_t)s * HD] * f;
   }
-  T* out = reinterpret_cast<T*>(a.out) + (size_t)r * a.ld_out + (size_t)head * HD + lane * DPL;
-#pragma unroll
-  for (int d = 0; d < DPL; ++d) {
-    const float y = L == 0.f ? 0.f : x[d] / L;
-    if constexpr (sizeof(T) == 4)
-      out[d] = y;
-    else
-      out[d] = Io<T>::from_f(y);
-  }
-  if (lane == 0 && a.lse) a.lse[(size_t)r * a.n_q + head] = L == 0.f ? -INFINITY : (M - kPShift + log2f(L)) * kLn2;
+  const float y = sum == 0.f ? 0.f : x / sum;
+  T* out = reinterpret_cast<T*>(a.out) + (size_t)r * a.ld_out + (size_t)head * HD + threadIdx.x;
+  if constexpr (sizeof(T) == 4)
+    *out = y;
+  else
+    *out = Io<T>::from_f(y);
+  if (threadIdx.x == 0 && a.lse) a.lse[(size_t)r * a.n_q + head] = lse_of(M, sum);
 }
 
 // ---------------------------------------------------------------- accumulated weights
 
 constexpr int kWWarps = 8;
-constexpr int kWQ = 8;  // queries staged at once are kWQ eights
+constexpr int kWEights = 8;  // eights of queries staged at once
 
-// Grid (groups of kWWarps tiles, KV heads): each warp owns one sixteen-slot tile, the CTA walks over the
-// chosen queries.
+// Grid (CTAs, KV heads).  The CTA stages up to 64 chosen queries, then its warps walk over their sixteen-slot tiles:
+// a tile's K is converted once, in registers, while the next tile's is on its way, and multiplied by every eight.
+// More queries go round again (their K comes from L2); a slot's sum stays with one lane pair throughout.
 template <typename T, int HD, int CODE>
-__global__ void __launch_bounds__(kWWarps * 32) k_kv8_weights(const __grid_constant__ Kv8AttnArgs a, int n_slots) {
+__global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_constant__ Kv8AttnArgs a, int n_slots) {
   constexpr bool SPLIT = sizeof(T) == 4;
-  constexpr int NJ = HD / 64;
+  constexpr int NJ = HD / 64, STEPS = HD / 16;
   constexpr int QW = HD / 16 * 64;
-  extern __shared__ uint32_t smem[];
+  extern __shared__ __align__(16) uint32_t smem[];
   uint32_t* s_hi = smem;
-  uint32_t* s_lo = smem + kWQ * QW;
-  __shared__ float s_coef[kWQ * 8], s_lse[kWQ * 8];
-  __shared__ unsigned long long s_mask[kWQ * 8];
+  uint32_t* s_lo = smem + kWEights * QW;
+  __shared__ float s_coef[kWEights * 8], s_lse[kWEights * 8];
+  __shared__ unsigned long long s_mask[kWEights * 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int h = blockIdx.y;
-  const int slot0 = (blockIdx.x * kWWarps + warp) * 16;
   const bool cap = a.cap > 0.f;
-  const bool full = slot0 + 16 <= a.prefix;
-  const bool some = slot0 < a.prefix || (slot0 < a.base + a.rows && slot0 + 16 > a.base);
-  const int page = slot0 < n_slots && some ? a.c.btab[slot0 / kPage] : -1;
-  const bool live = a.c.page_ok(page);
-  uint4 klo[NJ], khi[NJ];
-  float ks = 0.f;
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) klo[j] = khi[j] = make_uint4(0u, 0u, 0u, 0u);
-  if (live) {
-    const size_t row0 = a.c.page_row(page, h) + (size_t)(slot0 % kPage) * HD;
+  const int n_tiles = (n_slots + 15) >> 4, stride = gridDim.x * kWWarps;
+  const int first = blockIdx.x * kWWarps + warp;
+  const int nq = a.n_take * a.group;
+
+  // Page of tile ti, or -1 where it has none or no row sees it.
+  auto page_of = [&](int ti) {
+    if (ti >= n_tiles || !visible_any(ti * 16, a)) return -1;
+    const int page = __ldg(a.c.btab + ti * 16 / kPage);
+    return a.c.page_ok(page) ? page : -1;
+  };
+  struct Tile {
+    uint4 lo[NJ], hi[NJ];  // codes of rows g and g + 8
+    float ks;
+    bool live;
+  };
+  auto load = [&](Tile& t, int ti, int page) {
+    t.live = page >= 0;
+    if (!t.live) return;
+    const int in_page = ti * 16 % kPage;
+    const size_t row0 = a.c.page_row(page, h) + (size_t)(in_page + g) * HD + c * 16;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      klo[j] = ld16(a.c.k + row0 + (size_t)g * HD + (c + 4 * j) * 16);
-      khi[j] = ld16(a.c.k + row0 + (size_t)(g + 8) * HD + (c + 4 * j) * 16);
+      t.lo[j] = ld16(a.c.k + row0 + j * 64);
+      t.hi[j] = ld16(a.c.k + row0 + 8 * HD + j * 64);
     }
-    ks = __ldg(a.c.ks + a.c.scale_at(page, h, slot0 % kPage));
-  }
-  float sum[2] = {0.f, 0.f};  // slots g and g + 8
-  const int nq = a.n_take * a.group;
-  for (int q0 = 0; q0 < nq; q0 += kWQ * 8) {
-    const int eights = min(kWQ, (nq - q0 + 7) / 8);
-    __syncthreads();
+    t.ks = __ldg(a.c.ks + a.c.scale_at(page, h, in_page));
+  };
+
+  for (int q0 = 0; q0 == 0 || q0 < nq; q0 += kWEights * 8) {
+    const int eights = nq ? min(kWEights, (nq - q0 + 7) / 8) : 0;
+    Tile cur;
+    load(cur, first, page_of(first));
+    int page = page_of(first + stride);
+    if (q0) __syncthreads();
     for (int q = warp; q < eights * 8; q += kWWarps) {
       const int qi = q0 + q;
       const T* p = nullptr;
@@ -473,73 +743,116 @@ __global__ void __launch_bounds__(kWWarps * 32) k_kv8_weights(const __grid_const
       }
     }
     __syncthreads();
-    if (!live) continue;
-    for (int t = 0; t < eights; ++t) {
-      float s[1][4] = {{0.f, 0.f, 0.f, 0.f}};
-      scores<HD, CODE, SPLIT, 1>(s, klo, khi, s_hi + t * QW, s_lo + t * QW, lane);
+
+    for (int ti = first; ti < n_tiles; ti += stride) {
+      const int slot0 = ti * 16;
+      float sum[2] = {0.f, 0.f};  // slots g and g + 8
+      const bool live = cur.live;
+      const float ks = cur.ks;
+      uint32_t k[STEPS][4];
+      if (live) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int q = t * 8 + 2 * c + (e & 1);
-        const float cf = s_coef[q] * ks;
-        const float x = cap ? capped(s[0][e], cf, a.cap) - s_lse[q] : fmaf(s[0][e], cf, -s_lse[q]);
-        const bool see = full || visible(slot0 + g + (e >> 1) * 8, a.prefix, a.base, s_mask[q]);
-        sum[e >> 1] += see ? exp2_approx(x) : 0.f;
+        for (int i = 0; i < STEPS; ++i) {
+          codes_to_half<CODE>(word_of(cur.lo[i >> 2], i & 3), k[i][0], k[i][2]);
+          codes_to_half<CODE>(word_of(cur.hi[i >> 2], i & 3), k[i][1], k[i][3]);
+        }
       }
-    }
-  }
+      load(cur, ti + stride, page);
+      page = page_of(ti + 2 * stride);
+      if (live) {
+        const bool full = slot0 + 16 <= a.prefix;
+        for (int t = 0; t < eights; ++t) {
+          float s[2][4] = {};
+          const uint32_t* hi = s_hi + t * QW + lane;
+          const uint32_t* lo = s_lo + t * QW + lane;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
-    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
-  }
-  if (c < 2) {
-    const int slot = slot0 + g + c * 8;
-    if (slot < n_slots) {
-      const size_t at = (size_t)h * a.ld_w + slot;
-      a.w_out[at] = (a.w_in ? a.w_in[at] : 0.f) + sum[c];
+          for (int i = 0; i < STEPS; ++i) {
+            mma16816(s[SPLIT ? 0 : i & 1], k[i], hi[i * 64], hi[i * 64 + 32]);
+            if (SPLIT) mma16816(s[1], k[i], lo[i * 64], lo[i * 64 + 32]);
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int q = t * 8 + 2 * c + u;
+            const float cf = s_coef[q] * ks, lse = s_lse[q];
+            const unsigned long long mask = full ? 0ull : s_mask[q];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float y = s[0][2 * r + u] + s[1][2 * r + u];
+              const float x = cap ? capped(y * cf, a.cap) - lse : fmaf(y, cf, -lse);
+              sum[r] += full || visible(slot0 + g + r * 8, a.prefix, a.base, mask) ? exp2_approx(x) : 0.f;
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+      }
+      const int slot = slot0 + g + c * 8;
+      if (c < 2 && slot < n_slots) {
+        const size_t at = (size_t)h * a.ld_w + slot;
+        a.w_out[at] = (q0 ? a.w_out[at] : a.w_in ? a.w_in[at] : 0.f) + (c ? sum[1] : sum[0]);
+      }
     }
   }
 }
 
 template <typename T, int HD, int CODE, int QT>
-bool run_attention(const Kv8AttnArgs& a, cudaStream_t st) {
-  constexpr int QB = 8 * QT;
-  constexpr size_t stage = (size_t)QT * (HD / 16 * 64) * 4 * (sizeof(T) == 4 ? 2 : 1);
-  constexpr size_t merge = (size_t)kAttnWarps * HD * (QB + 1) * 4;
-  constexpr size_t smem = stage > merge ? stage : merge;
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(k_kv8_attention<T, HD, CODE, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-          cudaSuccess)
-    return false;
+bool run_attention(Kv8AttnArgs a, cudaStream_t st) {
+  const Tiles<5> tiles(a.prefix, a.base, a.rows);
+  a.split_tiles = (tiles.n + a.n_split - 1) / a.n_split;
+  using L = AttnSmem<T, HD, QT>;
+  const auto kern = k_kv8_attention<T, HD, CODE, QT>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) != cudaSuccess) return false;
   const int nq = a.rows * a.group;
-  k_kv8_attention<T, HD, CODE, QT><<<dim3(a.n_split, a.c.n_kv, (nq + QB - 1) / QB), kAttnWarps * 32, smem, st>>>(a);
-  if (a.n_split > 1) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((a.c.n_kv * nq + 3) / 4);
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
-    cfg.attrs = attr;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(a.n_split, a.c.n_kv, (nq + L::QB - 1) / L::QB);
+  cfg.blockDim = dim3(L::W * 32);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 0;
+  if (!a.part_o && a.n_split > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.n_split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k_kv8_merge<T, HD>, a) != cudaSuccess) return false;
   }
-  return cudaGetLastError() == cudaSuccess;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return false;
+  if (!a.part_o) return true;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(a.c.n_kv * nq);
+  cfg.blockDim = dim3(HD);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_kv8_merge<T, HD>, a) == cudaSuccess;
 }
+
+// Query eights of a CTA: all of a KV head's queries up to four eights.
+int query_eights(int nq) { return nq <= 8 ? 1 : nq <= 16 ? 2 : nq <= 24 ? 3 : 4; }
 
 template <typename T, int HD, int CODE>
 bool run_attention_q(const Kv8AttnArgs& a, cudaStream_t st) {
-  return a.rows * a.group <= 8 ? run_attention<T, HD, CODE, 1>(a, st) : run_attention<T, HD, CODE, 2>(a, st);
+  switch (query_eights(a.rows * a.group)) {
+    case 1: return run_attention<T, HD, CODE, 1>(a, st);
+    case 2: return run_attention<T, HD, CODE, 2>(a, st);
+    case 3: return run_attention<T, HD, CODE, 3>(a, st);
+  }
+  return run_attention<T, HD, CODE, 4>(a, st);
 }
 
 template <typename T, int HD, int CODE>
 bool run_weights(const Kv8AttnArgs& a, cudaStream_t st) {
-  constexpr size_t smem = (size_t)kWQ * (HD / 16 * 64) * 4 * (sizeof(T) == 4 ? 2 : 1);
+  constexpr size_t smem = (size_t)kWEights * (HD / 16 * 64) * 4 * (sizeof(T) == 4 ? 2 : 1);
   const int n_slots = a.prefix > a.base + a.rows ? a.prefix : a.base + a.rows;
-  const int tiles = (n_slots + 15) / 16;
-  k_kv8_weights<T, HD, CODE>
-      <<<dim3((tiles + kWWarps - 1) / kWWarps, a.c.n_kv), kWWarps * 32, smem, st>>>(a, n_slots);
+  const int groups = ((n_slots + 15) / 16 + kWWarps - 1) / kWWarps;  // CTAs with a tile for every warp
+  int fit = 2 * 152 / a.c.n_kv;                                       // two CTAs on each of 152 SMs
+  if (fit < 1) fit = 1;
+  k_kv8_weights<T, HD, CODE><<<dim3(groups < fit ? groups : fit, a.c.n_kv), kWWarps * 32, smem, st>>>(a, n_slots);
   return cudaGetLastError() == cudaSuccess;
 }
 
@@ -560,14 +873,18 @@ bool weights_of(const Kv8AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-int kv8_attention_splits(int rows, int group, int n_kv, int slots) {
-  const int nq = rows * group;
-  const int blocks = n_kv * (nq <= 8 ? 1 : (nq + 15) / 16);
-  const int tiles = (slots + 15) / 16;
-  const int fit = 304 / blocks;                          // two CTAs on each of 152 SMs
-  const int most = (tiles + kAttnWarps - 1) / kAttnWarps;  // a tile for every warp
-  const int n = fit < most ? fit : most;
-  return n < 1 ? 1 : n;
+Kv8Splits kv8_attention_splits(int rows, int group, int n_kv, int slots) {
+  const int nq = rows * group, qb = 8 * query_eights(nq);
+  const int blocks = n_kv * ((nq + qb - 1) / qb);
+  const int tiles = (slots + kTileSlots - 1) / kTileSlots;
+  const int fit = kMaxSplits / blocks;                     // one CTA on each of 152 SMs
+  const int warps = qb == 8 ? 12 : 8;
+  const int most = (tiles + warps - 1) / warps;            // a tile for every warp
+  int n = fit < most ? fit : most;
+  if (n <= 1) return {1, false};
+  const int per = (tiles + n - 1) / n;
+  n = (tiles + per - 1) / per;                             // no split without a tile
+  return {n, n > kMaxCluster};
 }
 
 bool launch_kv8_attention(const Kv8AttnArgs& a, int io, cudaStream_t st) {

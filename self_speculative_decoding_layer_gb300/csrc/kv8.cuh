@@ -9,8 +9,6 @@
 // the softmax weights (V).
 #pragma once
 
-#include <cuda_fp8.h>
-
 #include "common.cuh"
 
 namespace ssd {
@@ -40,7 +38,7 @@ struct Kv8View {
 
 // D += A B, A 16x16 fp16 (row), B 16x8 fp16 (col), D 16x8 fp32.
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -49,7 +47,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // Transpose of an 8x8 matrix of 16-bit values held one row pair per lane.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
@@ -87,29 +85,50 @@ __device__ __forceinline__ void pair_to_half(uint32_t a, uint32_t b, uint32_t (&
   codes_to_half<CODE>(z23, h[2], h[3]);
 }
 
-// The value of a code before its scale.
-__device__ __forceinline__ float code_value(uint8_t c, int code) {
-  if (code == KV8_INT8) return (float)(int8_t)c;
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-  return __half2float(__half(h));
+// Values of the four codes of a word under scale s (fp32 products; |code| <= 448 is exact in fp16 and fp32).
+__device__ __forceinline__ void decode4(uint32_t w, float s, int code, float* x) {
+  uint32_t h01, h23;
+  if (code == KV8_INT8)
+    codes_to_half<KV8_INT8>(w, h01, h23);
+  else
+    codes_to_half<KV8_E4M3>(w, h01, h23);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+  x[0] = __fmul_rn(a.x, s), x[1] = __fmul_rn(a.y, s), x[2] = __fmul_rn(b.x, s), x[3] = __fmul_rn(b.y, s);
 }
 
-__device__ __forceinline__ float code_max(int code) { return code == KV8_INT8 ? 127.f : 448.f; }
-
-// Code of x under the inverse scale m: the fp32 product rounded to the nearest code (ties to even),
-// clamped to the largest one.  NaN becomes 0; the product of an infinity and m > 0 clamps.
-__device__ __forceinline__ uint8_t encode(float x, float m, int code) {
-  const float lim = code_max(code);
-  float y = m > 0.f && x == x ? __fmul_rn(x, m) : 0.f;
-  y = fminf(lim, fmaxf(-lim, y));
-  if (code == KV8_INT8) return (uint8_t)(int8_t)__float2int_rn(y);
-  return (uint8_t)__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+// Four codes, packed, of x under the inverse scale m: the fp32 products rounded to the nearest codes (ties to even),
+// clamped to the largest one.  NaN becomes 0; the product of an infinity and m > 0 clamps.  ODD: whether x may hold a
+// NaN or an infinity; without one |x m| rounds to qmax at most, since the scale is no smaller than the block's
+// largest magnitude over qmax.
+template <bool ODD>
+__device__ __forceinline__ uint32_t encode4(const float* x, float m, int code) {
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[i] = __fmul_rn(x[i], m);
+    if (ODD) {
+      const float lim = code == KV8_INT8 ? 127.f : 448.f;
+      y[i] = m > 0.f && x[i] == x[i] ? fminf(lim, fmaxf(-lim, y[i])) : 0.f;
+    }
+  }
+  if (code == KV8_INT8) {
+    // 1.5 2^23 + y: the sum's low byte is y rounded to the nearest integer, ties to even, in two's complement
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(__fadd_rn(y[i], 12582912.f));
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  }
+  uint16_t lo, hi;  // (cvt's first source is the upper half)
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
 // Scale of a block whose largest finite magnitude is amax (0 where that is below the smallest normal
 // number, so that its inverse is finite), and the inverse that its codes are taken with.
 __device__ __forceinline__ float block_scale(float amax, int code) {
-  const float s = __fdiv_rn(amax, code_max(code));
+  const float s = __fdiv_rn(amax, code == KV8_INT8 ? 127.f : 448.f);
   return s < 1.17549435e-38f ? 0.f : s;
 }
 __device__ __forceinline__ float inverse_scale(float s) { return s > 0.f ? __frcp_rn(s) : 0.f; }

@@ -34,8 +34,9 @@ struct Kv8AttnArgs {
   int prefix, base;
   float scale, cap;          // cap 0: none
   unsigned long long any;    // union of the masks
-  int n_split;               // key splits; more than one: partial results, merged by a second kernel
-  float* part_o;             // [n_kv * queries][n_split][hd]
+  int n_split;               // key splits
+  int split_tiles;           // tiles of a split (set by the launcher)
+  float* part_o;             // partial results for a second kernel, [n_kv * queries][n_split][hd]; null: none
   float2* part_ml;           // [n_kv * queries][n_split]: running maximum (log2) and sum
   // weights kernel
   const float* w_in;         // [n_kv][ld_w] or null
@@ -50,8 +51,13 @@ struct Kv8AttnArgs {
 bool launch_kv8_append(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st);
 bool launch_kv8_read(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st);
 bool launch_kv8_evict(const Kv8View& src, const Kv8View& dst, const Kv8SelectArgs& a, cudaStream_t st);
-// Key splits of an attention launch over `slots` slots.
-int kv8_attention_splits(int rows, int group, int n_kv, int slots);
+// Key splits of an attention launch over `slots` slots, and whether they merge through device scratch (else in
+// the distributed shared memory of a cluster).
+struct Kv8Splits {
+  int n;
+  bool scratch;
+};
+Kv8Splits kv8_attention_splits(int rows, int group, int n_kv, int slots);
 bool launch_kv8_attention(const Kv8AttnArgs& a, int io, cudaStream_t st);
 bool launch_kv8_weights(const Kv8AttnArgs& a, int io, cudaStream_t st);
 

@@ -87,9 +87,11 @@ bool attn_args(const ssd_kv8_cache* c, const ssd_kv8_attention_args* p, Kv8AttnA
 
 int slots_of(const Kv8AttnArgs& a) { return a.prefix > a.base + a.rows ? a.prefix : a.base + a.rows; }
 
-size_t part_bytes(const Kv8AttnArgs& a) {
-  if (a.n_split == 1) return 0;
-  return (size_t)a.c.n_kv * a.rows * a.group * a.n_split * (a.c.hd + 2) * 4;
+// Sets a's key splits; bytes of scratch that they need.
+size_t split(Kv8AttnArgs* a) {
+  const Kv8Splits s = kv8_attention_splits(a->rows, a->group, a->c.n_kv, slots_of(*a));
+  a->n_split = s.n;
+  return s.scratch ? (size_t)a->c.n_kv * a->rows * a->group * s.n * (a->c.hd + 2) * 4 : 0;
 }
 
 }  // namespace
@@ -111,8 +113,7 @@ ssd_status ssd_kv8_read(const ssd_kv8_cache* cache, const ssd_kv8_rows* rows, vo
 size_t ssd_kv8_attention_scratch_bytes(const ssd_kv8_cache* cache, const ssd_kv8_attention_args* args) {
   Kv8AttnArgs a{};
   if (!attn_args(cache, args, &a)) return 0;
-  a.n_split = kv8_attention_splits(a.rows, a.group, a.c.n_kv, slots_of(a));
-  const size_t b = part_bytes(a);
+  const size_t b = split(&a);
   return b < 256 ? 256 : (b + 255) / 256 * 256;
 }
 
@@ -123,10 +124,10 @@ ssd_status ssd_kv8_attention(const ssd_kv8_cache* cache, const ssd_kv8_attention
   if (!rows_ok(args->out, args->ld_out, (int64_t)a.n_q * a.c.hd, args->dtype)) return SSD_ERR_INVALID_ARG;
   a.out = args->out;
   a.ld_out = (size_t)args->ld_out;
-  a.n_split = kv8_attention_splits(a.rows, a.group, a.c.n_kv, slots_of(a));
-  if (a.n_split > 1) {
+  const size_t need = split(&a);
+  if (need) {
     if (!scratch || ((uintptr_t)scratch & 255)) return SSD_ERR_INVALID_ARG;
-    if (scratch_bytes < part_bytes(a)) return SSD_ERR_CAPACITY;
+    if (scratch_bytes < need) return SSD_ERR_CAPACITY;
     a.part_o = (float*)scratch;
     a.part_ml = (float2*)(a.part_o + (size_t)a.c.n_kv * a.rows * a.group * a.n_split * a.c.hd);
   }

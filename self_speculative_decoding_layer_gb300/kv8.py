@@ -7,7 +7,9 @@ from __future__ import annotations
 
 import ctypes
 import math
-from typing import Optional, Sequence, Tuple
+from typing import Optional, Sequence
+
+import torch
 
 from . import SSDError, KV8AttentionArgsC, KV8CacheC, KV8EvictArgsC, KV8RowsC, load_library
 
@@ -18,12 +20,12 @@ _CAUSAL = (ctypes.c_uint64 * MAX_ROWS)(*[(2 << r) - 1 for r in range(MAX_ROWS)])
 _CAUSAL_AT = ctypes.addressof(_CAUSAL)
 _MASK_AT = KV8AttentionArgsC.mask.offset
 _ref = ctypes.byref
-
-
-def _torch():
-    import torch
-
-    return torch
+_FLOAT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+# A call's time on the host is what bounds the small operators, so the current device and stream are asked for without
+# the objects that torch.cuda wraps them in (1 us less a call).
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+_empty = torch.empty
 
 
 class KVCache8:
@@ -35,7 +37,6 @@ class KVCache8:
     def __init__(self, n_layers: int, n_kv_heads: int, head_dim: int, max_tokens: int, dtype=None, block_tokens: int = 64,
                  device="cuda"):
         """An empty cache of ceil(max_tokens / 64) pages; dtype torch.int8 (the default) or torch.float8_e4m3fn."""
-        torch = _torch()
         dtype = torch.int8 if dtype is None else dtype
         if dtype not in (torch.int8, torch.float8_e4m3fn):
             raise SSDError(1, f"codes are torch.int8 or torch.float8_e4m3fn, not {dtype}")
@@ -56,7 +57,6 @@ class KVCache8:
         return c
 
     def _bind(self, k, v, k_scale, v_scale, block_table):
-        torch = _torch()
         if k.dtype not in (torch.int8, torch.float8_e4m3fn) or k.dim() != 5 or k.shape[3] != PAGE:
             raise SSDError(1, "k is [n_layers, pool_pages, n_kv_heads, 64, head_dim] of int8 or float8_e4m3fn")
         blocks = k_scale.shape[-1] if k_scale.dim() == 4 else 0
@@ -76,7 +76,7 @@ class KVCache8:
         self.n_pages, self.block_tokens = block_table.numel(), PAGE // blocks
         self.device = k.device
         self._lib = load_library()
-        self._float = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        self._index = k.get_device()
         code = 3 if k.dtype == torch.int8 else 4
         self._layers = [KV8CacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   block_table.data_ptr(), self.n_pages, self.pool_pages, i, self.n_kv_heads,
@@ -84,65 +84,63 @@ class KVCache8:
         self._scale = 1.0 / math.sqrt(self.head_dim)
 
     # -- plumbing
+    def _call(self, fn, *args):
+        """One C call on the current stream of the cache's device."""
+        index = self._index
+        if _device() != index:
+            with torch.cuda.device(index):
+                rc = fn(*args, _stream(index))
+        else:
+            rc = fn(*args, _stream(index))
+        if rc:
+            raise SSDError(rc, f"{fn.__name__} refused its arguments" if rc != 5 else fn.__name__)
+
     def _layer(self, layer: int) -> KV8CacheC:
         if not 0 <= layer < self.n_layers:
             raise SSDError(1, f"layer {layer} of {self.n_layers}")
         return self._layers[layer]
 
-    def _run(self, fn, *args):
-        """One C call on the current stream of the cache's device."""
-        torch = _torch()
-        index = self.device.index
-        if torch.cuda.current_device() != index:
-            with torch.cuda.device(index):
-                rc = fn(*args, torch.cuda.current_stream(index).cuda_stream)
-        else:
-            rc = fn(*args, torch.cuda.current_stream(index).cuda_stream)
-        if rc:
-            raise SSDError(rc, f"{fn.__name__} refused its arguments" if rc != 5 else fn.__name__)
-
-    def _rows_of(self, t, heads: int, what: str) -> Tuple[int, int]:
-        """(type, elements between rows) of a [rows, heads, head_dim] tensor whose rows are contiguous."""
-        hd = self.head_dim
-        io = self._float.get(t.dtype)
-        if io is None or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != hd or t.device != self.device:
+    def _ld(self, t, heads: int, what: str) -> int:
+        """Elements between the rows of a [rows, heads, head_dim] float tensor whose rows are contiguous."""
+        shape, hd = t.shape, self.head_dim
+        if len(shape) != 3 or shape[1] != heads or shape[2] != hd or t.dtype not in _FLOAT or t.get_device() != self._index:
             raise SSDError(1, f"{what} is [rows, {heads}, {hd}] of float32, bfloat16 or float16 on {self.device}")
-        stride = t.stride()
-        if stride[2] != 1 or (heads > 1 and stride[1] != hd):
+        ld, s1, s2 = t.stride()
+        if s2 != 1 or (s1 != hd and heads > 1):
             raise SSDError(1, f"the rows of {what} are contiguous")
-        return io, stride[0] if t.shape[0] > 1 else heads * hd
+        return ld if shape[0] > 1 else heads * hd
 
     # -- API
     def append(self, layer: int, k, v, first: int) -> None:
         """Quantise rows k, v [rows, n_kv_heads, head_dim] into slots first .. first + rows - 1 (RoPE applied)."""
-        io, ld_k = self._rows_of(k, self.n_kv_heads, "k")
-        io_v, ld_v = self._rows_of(v, self.n_kv_heads, "v")
-        if io_v != io or v.shape[0] != k.shape[0]:
+        ld_k, ld_v = self._ld(k, self.n_kv_heads, "k"), self._ld(v, self.n_kv_heads, "v")
+        rows = k.shape[0]
+        if v.dtype != k.dtype or v.shape[0] != rows:
             raise SSDError(1, "k and v have the same rows and type")
-        a = KV8RowsC(k.data_ptr(), v.data_ptr(), ld_k, ld_v, io, first, k.shape[0])
-        self._run(self._lib.ssd_kv8_append, _ref(self._layer(layer)), _ref(a))
+        a = KV8RowsC(k.data_ptr(), v.data_ptr(), ld_k, ld_v, _FLOAT[k.dtype], first, rows)
+        self._call(self._lib.ssd_kv8_append, _ref(self._layer(layer)), _ref(a))
 
-    def read(self, layer: int, first: int, rows: int, dtype=None):
+    def read(self, layer: int, first: int, rows: int, dtype=torch.float32):
         """The values (k, v), [rows, n_kv_heads, head_dim] each, of slots first .. first + rows - 1."""
-        torch = _torch()
-        dtype = torch.float32 if dtype is None else dtype
-        if dtype not in self._float or rows < 1:
+        if dtype not in _FLOAT or rows < 1:
             raise SSDError(1, "rows >= 1 of float32, bfloat16 or float16")
-        k, v = (torch.empty((rows, self.n_kv_heads, self.head_dim), dtype=dtype, device=self.device) for _ in range(2))
+        shape = (rows, self.n_kv_heads, self.head_dim)
+        k, v = _empty(shape, dtype=dtype, device=self.device), _empty(shape, dtype=dtype, device=self.device)
         ld = self.n_kv_heads * self.head_dim
-        a = KV8RowsC(k.data_ptr(), v.data_ptr(), ld, ld, self._float[dtype], first, rows)
-        self._run(self._lib.ssd_kv8_read, _ref(self._layer(layer)), _ref(a))
+        a = KV8RowsC(k.data_ptr(), v.data_ptr(), ld, ld, _FLOAT[dtype], first, rows)
+        self._call(self._lib.ssd_kv8_read, _ref(self._layer(layer)), _ref(a))
         return k, v
 
     def _attention_args(self, q, prefix, base, masks, scale, softcap) -> KV8AttentionArgsC:
-        if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % self.n_kv_heads:
+        shape = q.shape
+        if len(shape) != 3 or shape[1] < 1 or shape[1] % self.n_kv_heads:
             raise SSDError(1, f"q is [rows, heads, {self.head_dim}], its heads a multiple of {self.n_kv_heads}")
-        rows, heads = q.shape[0], q.shape[1]
-        io, ld = self._rows_of(q, heads, "q")
+        rows, heads, _ = shape
+        ld = self._ld(q, heads, "q")
         if not 1 <= rows <= MAX_ROWS:
             raise SSDError(1, f"{rows} rows: 1 to {MAX_ROWS}")
-        a = KV8AttentionArgsC(q.data_ptr(), None, None, ld, 0, io, heads, rows, prefix, prefix if base is None else base,
-                              self._scale if scale is None else scale, softcap)
+        a = KV8AttentionArgsC(q.data_ptr(), None, None, ld, ld, _FLOAT[q.dtype], heads, rows, prefix,
+                              prefix if base is None else base, self._scale if scale is None else scale, softcap)
         if masks is None:
             ctypes.memmove(ctypes.addressof(a) + _MASK_AT, _CAUSAL_AT, 8 * rows)
         else:
@@ -157,23 +155,41 @@ class KVCache8:
         < rows of masks[r].  base None: the new slots continue the prefix; masks None: causal (row r sees new slots
         0 .. r); scale None: 1 / sqrt(head_dim); softcap > 0: scores become softcap * tanh(score / softcap).  Returns
         out (like q), with return_lse also the rows' log-sum-exp [rows, n_q_heads] in fp32."""
-        torch = _torch()
         a = self._attention_args(q, prefix, base, masks, scale, softcap)
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        elif out.shape != q.shape or out.dtype != q.dtype:
-            raise SSDError(1, "out has the shape and type of q")
+            out = _empty(q.shape, dtype=q.dtype, device=self.device)
+            a.ld_out = a.n_q_heads * self.head_dim
+        else:
+            if out.shape != q.shape or out.dtype != q.dtype:
+                raise SSDError(1, "out has the shape and type of q")
+            a.ld_out = self._ld(out, a.n_q_heads, "out")
         a.out = out.data_ptr()
-        a.ld_out = self._rows_of(out, q.shape[1], "out")[1]
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device) if return_lse else None
-        if lse is not None:
+        lse = None
+        if return_lse:
+            lse = _empty((a.rows, a.n_q_heads), dtype=torch.float32, device=self.device)
             a.lse = lse.data_ptr()
-        c = self._layer(layer)
-        need = self._lib.ssd_kv8_attention_scratch_bytes(_ref(c), _ref(a))
-        # per call, from the current stream's pool: calls on other streams and captured graphs share none of it
-        scratch = torch.empty(need, dtype=torch.uint8, device=self.device) if need > 256 else None
-        self._run(self._lib.ssd_kv8_attention, _ref(c), _ref(a), None if scratch is None else scratch.data_ptr(), need)
+        c, ra = _ref(self._layer(layer)), _ref(a)
+        need = self._lib.ssd_kv8_attention_scratch_bytes(c, ra)
+        if need > 256:
+            # per call, from the current stream's pool: calls on other streams and captured graphs share none of it
+            scratch = _empty(need, dtype=torch.uint8, device=self.device)
+            self._call(self._lib.ssd_kv8_attention, c, ra, scratch.data_ptr(), need)
+        else:
+            self._call(self._lib.ssd_kv8_attention, c, ra, None, 0)
         return (out, lse) if return_lse else out
+
+    def _weight_ld(self, t, slots: int) -> int:
+        """Elements between the heads of a float32 [n_kv_heads, >= slots] tensor whose rows are contiguous."""
+        shape = t.shape
+        if len(shape) != 2 or shape[0] != self.n_kv_heads or shape[1] < slots or t.dtype != torch.float32 or \
+                t.get_device() != self._index:
+            raise SSDError(1, f"weights are float32 [{self.n_kv_heads}, {slots} or more] on {self.device}")
+        ld, s1 = t.stride()
+        if shape[0] == 1:
+            ld = shape[1]
+        if (s1 != 1 and shape[1] > 1) or ld < shape[1]:
+            raise SSDError(1, "the rows of weights are contiguous and apart")
+        return ld
 
     def weights(self, layer: int, q, lse, prefix: int, base: Optional[int] = None, masks: Optional[Sequence[int]] = None,
                 scale: Optional[float] = None, softcap: float = 0.0, rows: Optional[Sequence[int]] = None, weight=None,
@@ -182,21 +198,17 @@ class KVCache8:
         arguments are repeated here with the lse it returned, to weight [n_kv_heads, slots] (fp32; None: zeros).
         Written to out, else into weight, else to a new tensor, which is returned; only its first
         max(prefix, base + rows) columns are touched."""
-        torch = _torch()
         a = self._attention_args(q, prefix, base, masks, scale, softcap)
-        if lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != self.device:
+        if lse.shape != (a.rows, a.n_q_heads) or lse.dtype != torch.float32 or not lse.is_contiguous() or \
+                lse.get_device() != self._index:
             raise SSDError(1, "lse is the contiguous float32 [rows, heads] of the attention call")
         a.lse = lse.data_ptr()
+        slots = max(prefix, a.base + a.rows)
         if out is None:
-            out = weight if weight is not None else torch.empty(
-                (self.n_kv_heads, max(a.prefix, a.base + a.rows, 1)), dtype=torch.float32, device=self.device)
-        for t in (weight, out):
-            if t is None:
-                continue
-            if t.dim() != 2 or t.shape[0] != self.n_kv_heads or t.dtype != torch.float32 or t.device != self.device or \
-                    t.shape[1] < max(a.prefix, a.base + a.rows) or t.stride() != out.stride() or \
-                    (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-                raise SSDError(1, f"weights are float32 [{self.n_kv_heads}, slots], laid out alike, for every visible slot")
+            out = weight if weight is not None else _empty((self.n_kv_heads, slots), dtype=torch.float32, device=self.device)
+        ld = self._weight_ld(out, slots)
+        if weight is not None and weight is not out and self._weight_ld(weight, slots) != ld:
+            raise SSDError(1, "weight and out are laid out alike")
         take = (1 << a.rows) - 1
         if rows is not None:
             take = 0
@@ -204,9 +216,8 @@ class KVCache8:
                 if not 0 <= r < a.rows:
                     raise SSDError(1, f"row {r} of {a.rows}")
                 take |= 1 << r
-        ld = out.stride(0) if self.n_kv_heads > 1 else out.shape[1]
-        self._run(self._lib.ssd_kv8_weights, _ref(self._layer(layer)), _ref(a), take,
-                  None if weight is None else weight.data_ptr(), out.data_ptr(), ld)
+        self._call(self._lib.ssd_kv8_weights, _ref(self._layer(layer)), _ref(a), take,
+                    None if weight is None else weight.data_ptr(), out.data_ptr(), ld)
         return out
 
     def evict(self, layer: int, weight, keep: int, recent: int, to: "KVCache8", to_layer: int):
@@ -214,18 +225,12 @@ class KVCache8:
         keep - recent heaviest others; they move, in slot order, to slots [0, keep) of layer to_layer of `to`, whose
         first pages must be none that this layer's slots use.  Returns the kept slots [n_kv_heads, keep] (int32) and
         their weights."""
-        torch = _torch()
-        if weight.dim() != 2 or weight.shape[0] != self.n_kv_heads or weight.dtype != torch.float32 or \
-                weight.device != self.device or weight.shape[1] < 1 or \
-                (weight.shape[1] > 1 and weight.stride(1) != 1) or \
-                (weight.shape[0] > 1 and weight.stride(0) < weight.shape[1]):
-            raise SSDError(1, f"weight is float32 [{self.n_kv_heads}, slots] on {self.device}, its rows contiguous")
+        ld = self._weight_ld(weight, 1)
         n = weight.shape[1]
         if to.device != self.device or not 1 <= keep <= n or not 0 <= recent <= keep:
             raise SSDError(1, f"0 <= recent <= keep <= {n}, keep >= 1, caches on one device")
-        index = torch.empty((self.n_kv_heads, keep), dtype=torch.int32, device=self.device)
-        kept = torch.empty((self.n_kv_heads, keep), dtype=torch.float32, device=self.device)
-        a = KV8EvictArgsC(weight.data_ptr(), weight.stride(0) if self.n_kv_heads > 1 else n, index.data_ptr(),
-                          kept.data_ptr(), n, keep, recent)
-        self._run(self._lib.ssd_kv8_evict, _ref(self._layer(layer)), _ref(to._layer(to_layer)), _ref(a))
+        index = _empty((self.n_kv_heads, keep), dtype=torch.int32, device=self.device)
+        kept = _empty((self.n_kv_heads, keep), dtype=torch.float32, device=self.device)
+        a = KV8EvictArgsC(weight.data_ptr(), ld, index.data_ptr(), kept.data_ptr(), n, keep, recent)
+        self._call(self._lib.ssd_kv8_evict, _ref(self._layer(layer)), _ref(to._layer(to_layer)), _ref(a))
         return index, kept

@@ -155,6 +155,10 @@ ATTN = [  # rows, prefix, base - prefix, masks, hq, hkv, hd, code, block, io, ca
     (7, 301, 0, "causal", 32, 8, 128, "int8", 64, "fp32", 0.0),
     (17, 259, 0, "tree", 40, 40, 128, "e4m3", 16, "fp16", 30.0),
     (17, 300, 5, "tree", 16, 4, 64, "int8", 32, "bf16", 5.0),
+    (6, 300, 0, "causal", 8, 2, 64, "int8", 16, "fp32", 0.0),  # 17 to 24 queries for a KV head
+    (5, 900, 0, "tree", 8, 2, 128, "e4m3", 16, "fp32", 0.0),
+    (3, 2500, 0, "causal", 16, 4, 64, "int8", 32, "fp16", 0.0),  # 9 to 16
+    (8, 700, 0, "tree", 32, 8, 64, "e4m3", 64, "fp32", 0.0),  # 25 to 32
     (5, 200, 213, "own", 16, 2, 128, "e4m3", 64, "fp32", 0.0),  # the DP rows' slots, past the committed ones
     (64, 128, 0, "causal", 8, 8, 64, "int8", 32, "fp32", 0.0),
     (64, 1000, 0, "holes", 64, 8, 128, "int8", 64, "bf16", 0.0),

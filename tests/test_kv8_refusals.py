@@ -95,12 +95,14 @@ def test_bad_outputs_and_scratch(lib):
     c = cache()
     for bad in (dict(out=None), dict(out=A + 8), dict(ld_out=100)):
         assert lib.ssd_kv8_attention(ctypes.byref(c), ctypes.byref(attn(**bad)), A, 1 << 30, None) == INVALID, bad
-    a = attn(prefix=250, base=250)
+    c = cache(n_pages=4096, pool_pages=4096, n_kv_heads=1)
+    a = attn(prefix=200000, base=200000, n_q_heads=8)
     need = lib.ssd_kv8_attention_scratch_bytes(ctypes.byref(c), ctypes.byref(a))
-    assert need > 256  # several key splits
+    assert need > 256  # few heads, a long context: more key splits than a cluster holds
     assert lib.ssd_kv8_attention(ctypes.byref(c), ctypes.byref(a), None, need, None) == INVALID
     assert lib.ssd_kv8_attention(ctypes.byref(c), ctypes.byref(a), A + 16, need, None) == INVALID
     assert lib.ssd_kv8_attention(ctypes.byref(c), ctypes.byref(a), A, 1024, None) == CAPACITY
+    c = cache()
     for w_in, w_out, ld in ((A, None, 256), (A, A + 2, 256), (A + 1, A, 256), (A, A, 100)):
         assert lib.ssd_kv8_weights(ctypes.byref(c), ctypes.byref(attn()), 1, w_in, w_out, ld, None) == INVALID
     assert lib.ssd_kv8_weights(ctypes.byref(c), ctypes.byref(attn(lse=None)), 1, A, A, 256, None) == INVALID
