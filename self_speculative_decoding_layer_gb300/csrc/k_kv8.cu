@@ -17,7 +17,7 @@ namespace ssd {
 
 namespace {
 
-constexpr int kQuantThreads = 256;
+constexpr int kQuantThreads = 512;
 
 template <typename T>
 __device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
@@ -75,91 +75,72 @@ __device__ __forceinline__ float block_max(float a, float* red) {
   return a;
 }
 
-// A block holds T * hd / 16 sixteen-value chunks (64..512); a thread takes chunk threadIdx.x and, in the
-// largest block, chunk threadIdx.x + 256.
+// A block holds T * hd / 16 chunks of sixteen values (64..512), one for each thread.
 template <typename T>
-__global__ void __launch_bounds__(kQuantThreads) k_kv8_append(Kv8View c, Kv8RowsArgs a) {
+__global__ void __launch_bounds__(kQuantThreads, 3) k_kv8_append(Kv8View c, Kv8RowsArgs a) {
   __shared__ float red[kQuantThreads / 32];
   const int h = blockIdx.y, which = blockIdx.z;
-  const int tokens = 1 << c.tshift, rshift = c.hd == 128 ? 3 : 2;  // 2^rshift chunks a row
-  const int block = (a.first >> c.tshift) + blockIdx.x;
-  const int slot0 = block << c.tshift;
+  const int rshift = c.hd == 128 ? 3 : 2;  // 2^rshift chunks a row
+  const int slot0 = ((a.first >> c.tshift) + blockIdx.x) << c.tshift;
   const int page = c.btab[slot0 / kPage];
-  const T* src = reinterpret_cast<const T*>(which ? a.v : a.k) + (size_t)h * c.hd;
-  const size_t ld = which ? a.ld_v : a.ld_k;
-  float x[2][16];
-  bool mine[2];
+  const int t = threadIdx.x >> rshift, row = slot0 + t - a.first;
+  const bool fresh = row >= 0 && row < a.rows;
+  float x[16];
   float amax = 0.f, odd = 0.f;  // of the new rows
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int i = threadIdx.x + j * kQuantThreads;
-    const int t = i >> rshift, d = (i - (t << rshift)) * 16;
-    const int row = slot0 + t - a.first;
-    mine[j] = t < tokens && row < a.rows;
-    if (mine[j] && row >= 0) {
-      load16(src + (size_t)row * ld + d, x[j]);
-      amax16(x[j], amax, odd);
-    }
+  if (fresh) {
+    const T* src = reinterpret_cast<const T*>(which ? a.v : a.k) + (size_t)row * (which ? a.ld_v : a.ld_k);
+    load16(src + (size_t)h * c.hd + (threadIdx.x - (t << rshift)) * 16, x);
+    amax16(x, amax, odd);
   }
   if (!c.page_ok(page)) return;
-  uint8_t* codes = (which ? c.v : c.k) + c.page_row(page, h) + (size_t)(slot0 % kPage) * c.hd;
+  uint8_t* codes = (which ? c.v : c.k) + c.page_row(page, h) + (size_t)(slot0 % kPage) * c.hd + threadIdx.x * 16;
   float* scale = (which ? c.vs : c.ks) + c.scale_at(page, h, slot0 % kPage);
   float s_old = 0.f;
   if (slot0 < a.first) {  // slots before the new rows stay, under a scale no smaller than theirs
     s_old = *scale;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = threadIdx.x + j * kQuantThreads;
-      if (mine[j] && slot0 + (i >> rshift) < a.first) {
-        decode16(*reinterpret_cast<const uint4*>(codes + (size_t)i * 16), s_old, c.code, x[j]);
-        float unused = 0.f;
-        amax16(x[j], unused, odd);
-      }
+    if (row < 0) {
+      decode16(*reinterpret_cast<const uint4*>(codes), s_old, c.code, x);
+      float unused = 0.f;
+      amax16(x, unused, odd);
     }
   }
   // (the barriers also order every read of the kept codes and scale before the writes)
   const bool any_odd = __syncthreads_or(odd != odd);
-  if (any_odd) {
-    amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (mine[j] && slot0 + ((threadIdx.x + j * kQuantThreads) >> rshift) >= a.first) amax = finite_amax16(x[j], amax);
-  }
+  if (any_odd) amax = fresh ? finite_amax16(x, 0.f) : 0.f;
   amax = block_max(amax, red);
   const float s = fmaxf(block_scale(amax, c.code), s_old);
   const float m = inverse_scale(s);
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (mine[j])
-      *reinterpret_cast<uint4*>(codes + (size_t)(threadIdx.x + j * kQuantThreads) * 16) =
-          any_odd ? encode16<true>(x[j], m, c.code) : encode16<false>(x[j], m, c.code);
+  if (row < a.rows)
+    *reinterpret_cast<uint4*>(codes) = any_odd ? encode16<true>(x, m, c.code) : encode16<false>(x, m, c.code);
   if (threadIdx.x == 0) *scale = s;
 }
 
-// A thread's sixteen bytes of output: 4 fp32 or 8 16-bit values.
+// Grid (runs of sixteen slots that share a scale, K / V).  A thread makes sixteen bytes of output (4 fp32 or 8 16-bit
+// values) at a time.
 template <typename T>
 __global__ void __launch_bounds__(256) k_kv8_read(Kv8View c, Kv8RowsArgs a) {
   constexpr int N = 16 / sizeof(T);
   const int per_row = c.hd / N, per_slot = per_row * c.n_kv;
-  const int which = blockIdx.z;
-  const uint8_t* from = which ? c.v : c.k;
-  const float* scales = which ? c.vs : c.ks;
-  T* to = reinterpret_cast<T*>(which ? a.v : a.k);
+  const int which = blockIdx.y;
+  const int slot0 = ((a.first >> 4) + blockIdx.x) << 4;
+  const int page = c.btab[slot0 / kPage];
+  const bool ok = c.page_ok(page);
+  const int r0 = max(0, a.first - slot0), r1 = min(16, a.first + a.rows - slot0);
+  const uint8_t* from = (which ? c.v : c.k) + (ok ? c.page_row(page, 0) : 0) + (size_t)(slot0 % kPage) * c.hd;
+  const float* scales = (which ? c.vs : c.ks) + (ok ? c.scale_at(page, 0, slot0 % kPage) : 0);
+  T* to = reinterpret_cast<T*>(which ? a.v : a.k) + ((ptrdiff_t)slot0 - a.first) * (ptrdiff_t)(which ? a.ld_v : a.ld_k);
   const size_t ld = which ? a.ld_v : a.ld_k;
-  for (int row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    const int slot = a.first + row, page = c.btab[slot / kPage];
-    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < per_slot; i += gridDim.x * blockDim.x) {
-      const int h = i / per_row, d = (i - h * per_row) * N;
+  for (int i = threadIdx.x; i < per_slot; i += blockDim.x) {
+    const int h = i / per_row, d = (i - h * per_row) * N;
+    const uint8_t* p = from + (size_t)h * kPage * c.hd + d;
+    const float s = ok ? scales[(size_t)h << (6 - c.tshift)] : 0.f;
+#pragma unroll 4
+    for (int r = r0; r < r1; ++r) {
       float x[N];
 #pragma unroll
-      for (int e = 0; e < N; ++e) x[e] = 0.f;
-      if (c.page_ok(page)) {
-        const uint8_t* p = from + c.page_row(page, h) + (size_t)(slot % kPage) * c.hd + d;
-        const float s = scales[c.scale_at(page, h, slot % kPage)];
-#pragma unroll
-        for (int e = 0; e < N; e += 4) decode4(__ldg(reinterpret_cast<const uint32_t*>(p + e)), s, c.code, x + e);
-      }
-      T* o = to + (size_t)row * ld + (size_t)i * N;
+      for (int e = 0; e < N; e += 4)
+        decode4(ok ? __ldg(reinterpret_cast<const uint32_t*>(p + r * c.hd + e)) : 0u, s, c.code, x + e);
+      T* o = to + (size_t)r * ld + (size_t)i * N;
       if constexpr (sizeof(T) == 4) {
         *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
       } else {
@@ -177,7 +158,7 @@ __global__ void __launch_bounds__(256) k_kv8_read(Kv8View c, Kv8RowsArgs a) {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelCluster = 8;
-constexpr int kSelKeys = 16;     // keys that a thread holds in registers
+constexpr int kSelKeys = 8;      // keys that a thread holds in registers
 constexpr int kDigitBits = 11;   // 32 bits in rounds of 11, 11 and 10
 constexpr int kBins = 1 << kDigitBits;
 
@@ -188,27 +169,26 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (b >> 31) ? ~b : b | 0x80000000u;
 }
 
-// Sum of v over the threads before this one (and the total) by warps, in order.
-__device__ __forceinline__ int block_prefix(int v, int* sums, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+// Sum of v over the lanes up to this one.
+__device__ __forceinline__ int warp_prefix(int v) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += t;
+    const int t = __shfl_up_sync(0xffffffffu, v, o);
+    if ((int)(threadIdx.x & 31) >= o) v += t;
   }
-  if (lane == 31) sums[warp] = inc;
+  return v;
+}
+
+// Each warp's sum v (the same in its lanes): the sum over the warps before this one, and over all.
+__device__ __forceinline__ int warps_before(int v, int* sums, int& total) {
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) sums[warp] = v;
   __syncthreads();
-  int s = sums[lane];  // kSelWarps = 32
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += t;
-  }
+  const int s = warp_prefix(sums[threadIdx.x & 31]);  // (32 warps)
   total = __shfl_sync(0xffffffffu, s, 31);
   const int before = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
   __syncthreads();
-  return inc - v + (warp ? before : 0);
+  return warp ? before : 0;
 }
 
 // Grid (cluster CTAs, heads).  The keep - recent heaviest of slots [0, n - recent), the lowest slots among equal ones,
@@ -235,18 +215,18 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
     if (kept) kept[want + i] = w[cand + i];
   }
   if (want == 0) return;  // the same in every CTA of the cluster
-  // CTA r holds candidates [r span, (r + 1) span), in chunks of a thread each: chunk j of the CTA is the run of
-  // kSelThreads * kSelKeys candidates from j on, of which thread t has kSelKeys consecutive ones
+  // CTA r holds candidates [r span, (r + 1) span), in runs; a warp has 32 kSelKeys consecutive ones of a run, a lane
+  // every 32nd of them
   constexpr int RUN = kSelThreads * kSelKeys;
   const int span = (cand + nr - 1) / nr;
   const int i0 = min(cand, rank * span), i1 = min(cand, i0 + span);
+  const int mine = i0 + (tid >> 5) * 32 * kSelKeys + (tid & 31);
   float x[kSelKeys];
   auto load = [&](int run) {
-    const int at = i0 + run + tid * kSelKeys;
 #pragma unroll
-    for (int e = 0; e < kSelKeys; ++e) x[e] = at + e < i1 ? w[at + e] : 0.f;
+    for (int e = 0; e < kSelKeys; ++e) x[e] = mine + run + e * 32 < i1 ? __ldg(w + mine + run + e * 32) : 0.f;
   };
-  auto valid = [&](int run, int e) { return i0 + run + tid * kSelKeys + e < i1; };
+  auto valid = [&](int run, int e) { return mine + run + e * 32 < i1; };
   const int n_run = RELOAD ? (i1 - i0 + RUN - 1) / RUN * RUN : RUN;
   if (!RELOAD) load(0);
   uint32_t prefix = 0;  // the threshold's leading bits found so far
@@ -268,13 +248,16 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
     cl.sync();
     // two bins a thread, from the top one down; the bin where the count from the top reaches need
     int v[2] = {0, 0};
-    for (int r = 0; r < nr; ++r) {
-      const int* rh = cl.map_shared_rank(hs, r);
-      v[0] += rh[kBins - 1 - 2 * tid];
-      v[1] += rh[kBins - 2 - 2 * tid];
-    }
+#pragma unroll
+    for (int r = 0; r < kSelCluster; ++r)
+      if (r < nr) {
+        const int2 t = *reinterpret_cast<const int2*>(cl.map_shared_rank(hs, r) + kBins - 2 - 2 * tid);
+        v[0] += t.y;
+        v[1] += t.x;
+      }
     int total;
-    int above = block_prefix(v[0] + v[1], sums, total);
+    const int inc = warp_prefix(v[0] + v[1]);
+    int above = warps_before(__shfl_sync(0xffffffffu, inc, 31), sums, total) + inc - v[0] - v[1];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (above < need && above + v[e] >= need) {
@@ -289,51 +272,56 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
     // (hist[round & 1] is cleared again two rounds on: after every CTA has passed the next round's cluster barrier)
   }
   // prefix is the threshold's key; candidates above it are taken, and the first `need` equal ones.
-  int gt = 0, eq = 0;
-  for (int run = 0; run < n_run; run += RUN) {
-    if (RELOAD) load(run);
+  int gt = 0, eq = 0;  // of this warp
+  auto count = [&](int run) {
+    gt = eq = 0;
 #pragma unroll
     for (int e = 0; e < kSelKeys; ++e) {
       const uint32_t k = weight_key(x[e]);
-      gt += valid(run, e) && k > prefix;
-      eq += valid(run, e) && k == prefix;
+      gt += __popc(__ballot_sync(0xffffffffu, valid(run, e) && k > prefix));
+      eq += __popc(__ballot_sync(0xffffffffu, valid(run, e) && k == prefix));
     }
-  }
+  };
   if (tid < 2) s_count[tid] = 0;
   __syncthreads();
-  atomicAdd(&s_count[0], gt);
-  atomicAdd(&s_count[1], eq);
+  for (int run = 0; run < n_run; run += RUN) {
+    if (RELOAD) load(run);
+    count(run);
+    if ((tid & 31) == 0) {
+      atomicAdd(&s_count[0], gt);
+      atomicAdd(&s_count[1], eq);
+    }
+  }
   cl.sync();
   int base_gt = 0, base_eq = 0;  // in the CTAs before this one
-  for (int r = 0; r < rank; ++r) {
-    const int* c = cl.map_shared_rank(s_count, r);
-    base_gt += c[0];
-    base_eq += c[1];
-  }
+#pragma unroll
+  for (int r = 0; r < kSelCluster; ++r)
+    if (r < rank) {
+      const int* c = cl.map_shared_rank(s_count, r);
+      base_gt += c[0];
+      base_eq += c[1];
+    }
   for (int run = 0; run < n_run; run += RUN) {
     if (RELOAD) {
       load(run);
-      gt = eq = 0;
-#pragma unroll
-      for (int e = 0; e < kSelKeys; ++e) {
-        const uint32_t k = weight_key(x[e]);
-        gt += valid(run, e) && k > prefix;
-        eq += valid(run, e) && k == prefix;
-      }
+      count(run);
     }
     int tg, te;
-    int ng = base_gt + block_prefix(gt, sums, tg), ne = base_eq + block_prefix(eq, sums, te);
+    int ng = base_gt + warps_before(gt, sums, tg), ne = base_eq + warps_before(eq, sums, te);
+    const unsigned below = (1u << (tid & 31)) - 1;
 #pragma unroll
     for (int e = 0; e < kSelKeys; ++e) {
       const uint32_t k = weight_key(x[e]);
       const bool g = valid(run, e) && k > prefix, q = valid(run, e) && k == prefix;
-      if (g || (q && ne < need)) {
-        const int pos = ng + min(ne, need);
-        index[pos] = i0 + run + tid * kSelKeys + e;
+      const unsigned bg = __ballot_sync(0xffffffffu, g), bq = __ballot_sync(0xffffffffu, q);
+      const int eq_before = ne + __popc(bq & below);
+      if (g || (q && eq_before < need)) {
+        const int pos = ng + __popc(bg & below) + min(eq_before, need);
+        index[pos] = mine + run + e * 32;
         if (kept) kept[pos] = x[e];
       }
-      ng += g;
-      ne += q;
+      ng += __popc(bg);
+      ne += __popc(bq);
     }
     base_gt += tg;
     base_eq += te;
@@ -342,53 +330,37 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
 }
 
 // Grid (blocks of the kept slots, heads, K / V).
-__global__ void __launch_bounds__(kQuantThreads) k_kv8_gather(Kv8View src, Kv8View dst, const int* index, int keep) {
+__global__ void __launch_bounds__(kQuantThreads, 3) k_kv8_gather(Kv8View src, Kv8View dst, const int* index, int keep) {
   __shared__ float red[kQuantThreads / 32];
   const int h = blockIdx.y, which = blockIdx.z;
-  const int tokens = 1 << dst.tshift, rshift = dst.hd == 128 ? 3 : 2;
+  const int rshift = dst.hd == 128 ? 3 : 2;
   const int slot0 = blockIdx.x << dst.tshift;
   griddep_wait();
   const int page = dst.btab[slot0 / kPage];
-  const uint8_t* from = which ? src.v : src.k;
-  const float* from_scale = which ? src.vs : src.ks;
-  int slot[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int t = (threadIdx.x + j * kQuantThreads) >> rshift;
-    slot[j] = t < tokens && slot0 + t < keep ? index[(size_t)h * keep + slot0 + t] : -1;
-  }
-  float x[2][16];
+  const int t = threadIdx.x >> rshift;
+  const bool used = slot0 + t < keep;
+  float x[16];
   float amax = 0.f, odd = 0.f;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (slot[j] < 0) continue;
-    const int i = threadIdx.x + j * kQuantThreads, d = (i & ((1 << rshift) - 1)) * 16;
-    const int p = src.btab[slot[j] / kPage], in_page = slot[j] % kPage;
+  if (used) {
+    const int slot = __ldg(index + (size_t)h * keep + slot0 + t);
+    const int p = __ldg(src.btab + slot / kPage), in_page = slot % kPage;
     if (src.page_ok(p)) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(from + src.page_row(p, h) + (size_t)in_page * src.hd + d));
-      decode16(u, from_scale[src.scale_at(p, h, in_page)], src.code, x[j]);
+      const uint8_t* codes = (which ? src.v : src.k) + src.page_row(p, h) + (size_t)in_page * src.hd;
+      const float s = __ldg((which ? src.vs : src.ks) + src.scale_at(p, h, in_page));
+      decode16(__ldg(reinterpret_cast<const uint4*>(codes + (threadIdx.x - (t << rshift)) * 16)), s, src.code, x);
     } else {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[j][e] = 0.f;
+      for (int e = 0; e < 16; ++e) x[e] = 0.f;
     }
-    amax16(x[j], amax, odd);
+    amax16(x, amax, odd);
   }
   if (!dst.page_ok(page)) return;
   const bool any_odd = __syncthreads_or(odd != odd);
-  if (any_odd) {
-    amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (slot[j] >= 0) amax = finite_amax16(x[j], amax);
-  }
+  if (any_odd) amax = used ? finite_amax16(x, 0.f) : 0.f;
   amax = block_max(amax, red);
   const float s = block_scale(amax, dst.code), m = inverse_scale(s);
-  uint8_t* to = (which ? dst.v : dst.k) + dst.page_row(page, h) + (size_t)(slot0 % kPage) * dst.hd;
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (slot[j] >= 0)
-      *reinterpret_cast<uint4*>(to + (size_t)(threadIdx.x + j * kQuantThreads) * 16) =
-          any_odd ? encode16<true>(x[j], m, dst.code) : encode16<false>(x[j], m, dst.code);
+  uint8_t* to = (which ? dst.v : dst.k) + dst.page_row(page, h) + (size_t)(slot0 % kPage) * dst.hd + threadIdx.x * 16;
+  if (used) *reinterpret_cast<uint4*>(to) = any_odd ? encode16<true>(x, m, dst.code) : encode16<false>(x, m, dst.code);
   if (threadIdx.x == 0) (which ? dst.vs : dst.ks)[dst.scale_at(page, h, slot0 % kPage)] = s;
 }
 
@@ -397,8 +369,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_kv8_gather(Kv8View src, Kv8Vi
 bool launch_kv8_append(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st) {
   const int t0 = a.first >> c.tshift, t1 = (a.first + a.rows - 1) >> c.tshift;
   const dim3 grid(t1 - t0 + 1, c.n_kv, 2);
-  const int chunks = (c.hd / 16) << c.tshift;
-  const int threads = chunks < kQuantThreads ? chunks : kQuantThreads;
+  const int threads = (c.hd / 16) << c.tshift;
   if (io == 0)
     k_kv8_append<__nv_bfloat16><<<grid, threads, 0, st>>>(c, a);
   else if (io == 1)
@@ -411,7 +382,7 @@ bool launch_kv8_append(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStrea
 bool launch_kv8_read(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st) {
   const int per_slot = c.n_kv * c.hd / (io == 2 ? 4 : 8);
   const int threads = per_slot < 256 ? (per_slot + 31) / 32 * 32 : 256;
-  const dim3 grid((per_slot + threads - 1) / threads, a.rows < 32768 ? a.rows : 32768, 2);
+  const dim3 grid(((a.first + a.rows - 1) >> 4) - (a.first >> 4) + 1, 2);
   if (io == 0)
     k_kv8_read<__nv_bfloat16><<<grid, threads, 0, st>>>(c, a);
   else if (io == 1)
@@ -438,11 +409,10 @@ bool launch_kv8_evict(const Kv8View& src, const Kv8View& dst, const Kv8SelectArg
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, reload ? k_kv8_select<true> : k_kv8_select<false>, a) != cudaSuccess) return false;
-  const int chunks = (dst.hd / 16) << dst.tshift;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(((a.keep - 1) >> dst.tshift) + 1, src.n_kv, 2);
-  cfg.blockDim = dim3(chunks < kQuantThreads ? chunks : kQuantThreads);
+  cfg.blockDim = dim3((dst.hd / 16) << dst.tshift);
   return cudaLaunchKernelEx(&cfg, k_kv8_gather, src, dst, (const int*)a.index, a.keep) == cudaSuccess;
 }
 

@@ -84,19 +84,17 @@ __device__ __forceinline__ uint4 ld16(const uint8_t* p) {
   return r;
 }
 
-// Query element e (0..hd) of row q of the query block, as fp32.
-template <typename T>
-__device__ __forceinline__ float q_elem(const T* p, int e) {
-  if constexpr (sizeof(T) == 4)
-    return p[e];
-  else
-    return Io<T>::to_f(p[e]);
+// A pair of neighbouring query elements as fp32.
+__device__ __forceinline__ float2 load2(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
+__device__ __forceinline__ float2 load2(const __half* p) { return __half22float2(__ldg(reinterpret_cast<const __half2*>(p))); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
+  return __bfloat1622float2(__ldg(reinterpret_cast<const __nv_bfloat162*>(p)));
 }
 
-// Lay out eight queries as the MMA's B operand in shared memory: word (step, half, lane) holds the fp16 pair
-// that lane (column g = lane / 4, c = lane % 4) multiplies in k step `step`.  Lane c's k indices of step
-// 4 j + i are bytes 4 i .. 4 i + 3 of the row's sixteen-byte chunk c + 4 j.  One warp for each query;
-// returns its inverse scale.
+// Lay out a query as column `col` of the MMA's B operand in shared memory.  Lane (g, c) of the MMA multiplies column
+// g; its k indices of step 4 j + i are bytes 4 i .. 4 i + 3 of the row's sixteen-byte chunk c + 4 j.  The words (fp16
+// pairs) of two steps lie side by side, so that a lane reads them sixteen bytes at a time: word
+// ((step / 2) 32 + lane) 4 + (step % 2) 2 + half.  One warp for each query; returns its inverse scale.
 template <typename T, int HD, bool SPLIT>
 __device__ __forceinline__ float stage_query(const T* q, uint32_t* hi, uint32_t* lo, int col, int lane) {
   constexpr int EPL = HD / 32;  // elements per lane: pairs (2 lane + 64 i)
@@ -104,9 +102,10 @@ __device__ __forceinline__ float stage_query(const T* q, uint32_t* hi, uint32_t*
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL / 2; ++i) {
-    x[2 * i] = q ? q_elem(q, 64 * i + 2 * lane) : 0.f;
-    x[2 * i + 1] = q ? q_elem(q, 64 * i + 2 * lane + 1) : 0.f;
-    amax = fmaxf(amax, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+    const float2 v = q ? load2(q + 64 * i + 2 * lane) : make_float2(0.f, 0.f);
+    x[2 * i] = v.x;
+    x[2 * i + 1] = v.y;
+    amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
   }
   amax = warp_max(amax);
   // a power of two that brings the largest magnitude into [128, 256)
@@ -122,7 +121,7 @@ __device__ __forceinline__ float stage_query(const T* q, uint32_t* hi, uint32_t*
     const int e = 64 * i + 2 * lane;  // even element of the pair
     const int chunk = e >> 4, word = (e >> 2) & 3, half = (e >> 1) & 1;
     const int step = (chunk >> 2) * 4 + word;
-    const int at = (step * 2 + half) * 32 + col * 4 + (chunk & 3);
+    const int at = ((step >> 1) * 32 + col * 4 + (chunk & 3)) * 4 + (step & 1) * 2 + half;
     const float a = x[2 * i] * f, b = x[2 * i + 1] * f;
     const uint32_t h = pack_half2(a, b);
     hi[at] = h;
@@ -133,24 +132,42 @@ __device__ __forceinline__ float stage_query(const T* q, uint32_t* hi, uint32_t*
 
 __device__ __forceinline__ uint32_t word_of(const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
 
-// S^T += K Q^T for sixteen keys (klo: rows g, khi: rows g + 8) and eight queries per QT; query(t, i) is the fp16
-// pair of word i of operand t that this lane multiplies (hi words, then lo words).
-template <int HD, int CODE, bool SPLIT, int QT, typename Query>
-__device__ __forceinline__ void scores(float (&s)[QT][4], const uint4 (&klo)[HD / 64], const uint4 (&khi)[HD / 64],
-                                       const Query& query) {
-  constexpr int STEPS = HD / 16;
+// S^T = K Q^T for two halves of sixteen keys (klo: rows g, khi: rows g + 8) and QT columns of eight queries.
+template <int HD, int CODE, bool SPLIT, int QT>
+__device__ __forceinline__ void scores(float (&s)[2][QT][4], const uint4 (&klo)[2][HD / 64], const uint4 (&khi)[2][HD / 64],
+                                       const uint32_t* qhi, const uint32_t* qlo, int lane) {
+  constexpr int QW = HD / 16 * 64;  // words of one eight-query operand
 #pragma unroll
-  for (int j = 0; j < HD / 64; ++j) {
+  for (int b = 0; b < 2; ++b)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t a[4];
-      codes_to_half<CODE>(word_of(klo[j], i), a[0], a[2]);
-      codes_to_half<CODE>(word_of(khi[j], i), a[1], a[3]);
-      const int step = 4 * j + i;
+    for (int t = 0; t < QT; ++t)
 #pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        mma16816(s[t], a, query(t, 2 * step), query(t, 2 * step + 1));
-        if (SPLIT) mma16816(s[t], a, query(t, 2 * (STEPS + step)), query(t, 2 * (STEPS + step) + 1));
+      for (int e = 0; e < 4; ++e) s[b][t][e] = 0.f;
+#pragma unroll
+  for (int p = 0; p < HD / 32; ++p) {  // pairs of k steps
+    uint32_t a[2][2][4];               // [step of the pair][half]
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        codes_to_half<CODE>(word_of(klo[b][p >> 1], (p & 1) * 2 + i), a[i][b][0], a[i][b][2]);
+        codes_to_half<CODE>(word_of(khi[b][p >> 1], (p & 1) * 2 + i), a[i][b][1], a[i][b][3]);
+      }
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      const uint4 h = *reinterpret_cast<const uint4*>(qhi + t * QW + (p * 32 + lane) * 4);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        mma16816(s[b][t], a[0][b], h.x, h.y);
+        mma16816(s[b][t], a[1][b], h.z, h.w);
+      }
+      if (SPLIT) {
+        const uint4 l = *reinterpret_cast<const uint4*>(qlo + t * QW + (p * 32 + lane) * 4);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          mma16816(s[b][t], a[0][b], l.x, l.y);
+          mma16816(s[b][t], a[1][b], l.z, l.w);
+        }
       }
     }
   }
@@ -289,6 +306,7 @@ __global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(
   for (int i = 0; i < R::kStages - 1; ++i) fill(i, t_first + warp + i * W, pages[i]);
   int page_next = pages[R::kStages - 1];
 
+#pragma unroll 4
   for (int q = warp; q < QB; q += W) {
     const int qi = q0 + q;
     const T* p = nullptr;
@@ -320,18 +338,6 @@ __global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][d][e] = 0.f;
 
-  // The staged queries: in registers for eight of them, else read again for every tile.
-  constexpr int QWORDS = HD / 8 * (SPLIT ? 2 : 1);
-  uint32_t qreg[QT == 1 ? QWORDS : 1];
-  if constexpr (QT == 1) {
-#pragma unroll
-    for (int i = 0; i < QWORDS; ++i) qreg[i] = s_hi[i * 32 + lane];
-  }
-  auto query = [&](int t, int i) -> uint32_t {
-    if constexpr (QT == 1) return qreg[i];
-    return i < HD / 8 ? s_hi[t * QW + i * 32 + lane] : s_lo[t * QW + (i - HD / 8) * 32 + lane];
-  };
-
   int st = 0;
   for (int ti = t_first + warp; ti < t_last; ti += W) {
     cp_async_wait<R::kStages - 2>();
@@ -357,14 +363,7 @@ __global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(
         khi[b][j] = *reinterpret_cast<const uint4*>(kbuf + R::at(b * 16 + g + 8, (c + 4 * j) * 16));
       }
     float s[2][QT][4];  // halves of sixteen keys
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-#pragma unroll
-      for (int t = 0; t < QT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[b][t][e] = 0.f;
-      scores<HD, CODE, SPLIT, QT>(s[b], klo[b], khi[b], query);
-    }
+    scores<HD, CODE, SPLIT, QT>(s, klo, khi, s_hi, s_lo, lane);
 
     const bool full = slot0 + kTileSlots <= a.prefix;
     float vmax = fmaxf(head.vs[0], head.vs[1]);
@@ -723,6 +722,7 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
     load(cur, first, page_of(first));
     int page = page_of(first + stride);
     if (q0) __syncthreads();
+#pragma unroll 4
     for (int q = warp; q < eights * 8; q += kWWarps) {
       const int qi = q0 + q;
       const T* p = nullptr;
@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
       if (qi < nq) {
         const int ti = qi / a.group, r = a.take[ti], head = h * a.group + qi - ti * a.group;
         p = reinterpret_cast<const T*>(a.q) + (size_t)r * a.ld_q + (size_t)head * HD;
-        lse = a.lse[(size_t)r * a.n_q + head];
+        lse = __ldg(a.lse + (size_t)r * a.n_q + head);
         mask = a.mask[r];
       }
       const float inv = stage_query<T, HD, SPLIT>(p, s_hi + (q >> 3) * QW, s_lo + (q >> 3) * QW, q & 7, lane);
@@ -763,12 +763,16 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
         const bool full = slot0 + 16 <= a.prefix;
         for (int t = 0; t < eights; ++t) {
           float s[2][4] = {};
-          const uint32_t* hi = s_hi + t * QW + lane;
-          const uint32_t* lo = s_lo + t * QW + lane;
 #pragma unroll
-          for (int i = 0; i < STEPS; ++i) {
-            mma16816(s[SPLIT ? 0 : i & 1], k[i], hi[i * 64], hi[i * 64 + 32]);
-            if (SPLIT) mma16816(s[1], k[i], lo[i * 64], lo[i * 64 + 32]);
+          for (int p = 0; p < STEPS / 2; ++p) {
+            const uint4 hi = *reinterpret_cast<const uint4*>(s_hi + t * QW + (p * 32 + lane) * 4);
+            mma16816(s[0], k[2 * p], hi.x, hi.y);
+            mma16816(s[SPLIT ? 0 : 1], k[2 * p + 1], hi.z, hi.w);
+            if (SPLIT) {
+              const uint4 lo = *reinterpret_cast<const uint4*>(s_lo + t * QW + (p * 32 + lane) * 4);
+              mma16816(s[1], k[2 * p], lo.x, lo.y);
+              mma16816(s[1], k[2 * p + 1], lo.z, lo.w);
+            }
           }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
