@@ -66,71 +66,97 @@ __device__ __forceinline__ float finite_amax16(const float (&x)[16], float a) {
   return a;
 }
 
-__device__ __forceinline__ float block_max(float a, float* red) {
-  a = warp_max(a);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+// The largest of two non-negative magnitudes over the CTA; true if odd is NaN in any thread.
+__device__ __forceinline__ bool block_max2(float& a, float& b, float odd, uint32_t (&red)[3][32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  // (magnitudes order like their bits)
+  const uint32_t x = __reduce_max_sync(0xffffffffu, __float_as_uint(a));
+  const uint32_t y = __reduce_max_sync(0xffffffffu, __float_as_uint(b));
+  const bool o = __any_sync(0xffffffffu, odd != odd);
+  if (lane == 0) red[0][warp] = x, red[1][warp] = y, red[2][warp] = o;
   __syncthreads();
-  a = red[0];
-  for (int w = 1; w < (int)(blockDim.x >> 5); ++w) a = fmaxf(a, red[w]);
-  return a;
+  a = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < warps ? red[0][lane] : 0u));
+  b = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < warps ? red[1][lane] : 0u));
+  return __any_sync(0xffffffffu, lane < warps && red[2][lane]);
 }
 
-// A block holds T * hd / 16 chunks of sixteen values (64..512), one for each thread.
+// Quantise a block of K (x[0], magnitudes up to amax[0]) and of V (x[1]): a chunk of sixteen values for each thread
+// with `used`, whose scales come from those with `counts` and are no smaller than least; write scales and codes.
+__device__ __forceinline__ void quantise(const float (&x)[2][16], float (&amax)[2], float odd, bool counts, bool used,
+                                         const float (&least)[2], int code, uint8_t* const (&to)[2], float* const (&scale)[2],
+                                         uint32_t (&red)[3][32]) {
+  // (the barrier also orders every read of kept codes and scales before the writes)
+  const bool any_odd = block_max2(amax[0], amax[1], odd, red);
+  if (any_odd) {
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 2; ++w) amax[w] = counts ? finite_amax16(x[w], 0.f) : 0.f;
+    block_max2(amax[0], amax[1], 0.f, red);
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const float s = fmaxf(block_scale(amax[w], code), least[w]);
+    const float m = inverse_scale(s);
+    if (used) *reinterpret_cast<uint4*>(to[w]) = any_odd ? encode16<true>(x[w], m, code) : encode16<false>(x[w], m, code);
+    if (threadIdx.x == 0) *scale[w] = s;
+  }
+}
+
+// Grid (blocks of T tokens, KV heads).  A block holds T * hd / 16 chunks of sixteen values (64..512) of K and of V, one
+// of each for every thread.
 template <typename T>
-__global__ void __launch_bounds__(kQuantThreads, 3) k_kv8_append(Kv8View c, Kv8RowsArgs a) {
-  __shared__ float red[kQuantThreads / 32];
-  const int h = blockIdx.y, which = blockIdx.z;
+__global__ void __launch_bounds__(kQuantThreads, 2) k_kv8_append(Kv8View c, Kv8RowsArgs a) {
+  __shared__ uint32_t red[3][32];
+  const int h = blockIdx.y;
   const int rshift = c.hd == 128 ? 3 : 2;  // 2^rshift chunks a row
   const int slot0 = ((a.first >> c.tshift) + blockIdx.x) << c.tshift;
   const int page = c.btab[slot0 / kPage];
   const int t = threadIdx.x >> rshift, row = slot0 + t - a.first;
   const bool fresh = row >= 0 && row < a.rows;
-  float x[16];
-  float amax = 0.f, odd = 0.f;  // of the new rows
+  float x[2][16];
+  float amax[2] = {0.f, 0.f}, odd = 0.f;  // of the new rows
   if (fresh) {
-    const T* src = reinterpret_cast<const T*>(which ? a.v : a.k) + (size_t)row * (which ? a.ld_v : a.ld_k);
-    load16(src + (size_t)h * c.hd + (threadIdx.x - (t << rshift)) * 16, x);
-    amax16(x, amax, odd);
+    const size_t at = (size_t)h * c.hd + (threadIdx.x - (t << rshift)) * 16;
+    load16(reinterpret_cast<const T*>(a.k) + (size_t)row * a.ld_k + at, x[0]);
+    load16(reinterpret_cast<const T*>(a.v) + (size_t)row * a.ld_v + at, x[1]);
+    amax16(x[0], amax[0], odd);
+    amax16(x[1], amax[1], odd);
   }
   if (!c.page_ok(page)) return;
-  uint8_t* codes = (which ? c.v : c.k) + c.page_row(page, h) + (size_t)(slot0 % kPage) * c.hd + threadIdx.x * 16;
-  float* scale = (which ? c.vs : c.ks) + c.scale_at(page, h, slot0 % kPage);
-  float s_old = 0.f;
+  const size_t at = c.page_row(page, h) + (size_t)(slot0 % kPage) * c.hd + threadIdx.x * 16;
+  const size_t sc = c.scale_at(page, h, slot0 % kPage);
+  float least[2] = {0.f, 0.f};
   if (slot0 < a.first) {  // slots before the new rows stay, under a scale no smaller than theirs
-    s_old = *scale;
+    least[0] = c.ks[sc];
+    least[1] = c.vs[sc];
     if (row < 0) {
-      decode16(*reinterpret_cast<const uint4*>(codes), s_old, c.code, x);
       float unused = 0.f;
-      amax16(x, unused, odd);
+      decode16(*reinterpret_cast<const uint4*>(c.k + at), least[0], c.code, x[0]);
+      decode16(*reinterpret_cast<const uint4*>(c.v + at), least[1], c.code, x[1]);
+      amax16(x[0], unused, odd);
+      amax16(x[1], unused, odd);
     }
   }
-  // (the barriers also order every read of the kept codes and scale before the writes)
-  const bool any_odd = __syncthreads_or(odd != odd);
-  if (any_odd) amax = fresh ? finite_amax16(x, 0.f) : 0.f;
-  amax = block_max(amax, red);
-  const float s = fmaxf(block_scale(amax, c.code), s_old);
-  const float m = inverse_scale(s);
-  if (row < a.rows)
-    *reinterpret_cast<uint4*>(codes) = any_odd ? encode16<true>(x, m, c.code) : encode16<false>(x, m, c.code);
-  if (threadIdx.x == 0) *scale = s;
+  quantise(x, amax, odd, fresh, row < a.rows, least, c.code, {c.k + at, c.v + at}, {c.ks + sc, c.vs + sc}, red);
 }
 
-// Grid (runs of sixteen slots that share a scale, K / V).  A thread makes sixteen bytes of output (4 fp32 or 8 16-bit
+// Grid (runs of `run` slots, a divisor of sixteen, so that they share a scale; K / V; parts of a row).  A thread makes sixteen bytes of output (4 fp32 or 8 16-bit
 // values) at a time.
 template <typename T>
-__global__ void __launch_bounds__(256) k_kv8_read(Kv8View c, Kv8RowsArgs a) {
+__global__ void __launch_bounds__(256) k_kv8_read(Kv8View c, Kv8RowsArgs a, int run) {
   constexpr int N = 16 / sizeof(T);
   const int per_row = c.hd / N, per_slot = per_row * c.n_kv;
   const int which = blockIdx.y;
-  const int slot0 = ((a.first >> 4) + blockIdx.x) << 4;
+  const int slot0 = (a.first / run + blockIdx.x) * run;
   const int page = c.btab[slot0 / kPage];
   const bool ok = c.page_ok(page);
-  const int r0 = max(0, a.first - slot0), r1 = min(16, a.first + a.rows - slot0);
+  const int r0 = max(0, a.first - slot0), r1 = min(run, a.first + a.rows - slot0);
   const uint8_t* from = (which ? c.v : c.k) + (ok ? c.page_row(page, 0) : 0) + (size_t)(slot0 % kPage) * c.hd;
   const float* scales = (which ? c.vs : c.ks) + (ok ? c.scale_at(page, 0, slot0 % kPage) : 0);
   T* to = reinterpret_cast<T*>(which ? a.v : a.k) + ((ptrdiff_t)slot0 - a.first) * (ptrdiff_t)(which ? a.ld_v : a.ld_k);
   const size_t ld = which ? a.ld_v : a.ld_k;
-  for (int i = threadIdx.x; i < per_slot; i += blockDim.x) {
+  const int i = blockIdx.z * blockDim.x + threadIdx.x;
+  if (i < per_slot) {
     const int h = i / per_row, d = (i - h * per_row) * N;
     const uint8_t* p = from + (size_t)h * kPage * c.hd + d;
     const float s = ok ? scales[(size_t)h << (6 - c.tshift)] : 0.f;
@@ -231,7 +257,7 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
   if (!RELOAD) load(0);
   uint32_t prefix = 0;  // the threshold's leading bits found so far
   int need = want;      // candidates still to take among those that share them
-#pragma unroll
+#pragma unroll 1
   for (int round = 0; round < 3; ++round) {
     const int bits = round == 2 ? 10 : kDigitBits, shift = round == 0 ? 21 : round == 1 ? 10 : 0;
     int* hs = hist[round & 1];
@@ -329,46 +355,56 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
   cl.sync();  // no CTA leaves while another may read its counters
 }
 
-// Grid (blocks of the kept slots, heads, K / V).
-__global__ void __launch_bounds__(kQuantThreads, 3) k_kv8_gather(Kv8View src, Kv8View dst, const int* index, int keep) {
-  __shared__ float red[kQuantThreads / 32];
-  const int h = blockIdx.y, which = blockIdx.z;
+// Grid (blocks of the kept slots, heads).
+template <int CODE>
+__global__ void __launch_bounds__(kQuantThreads, 2) k_kv8_gather(Kv8View src, Kv8View dst, const int* index, int keep) {
+  __shared__ uint32_t red[3][32];
+  const int h = blockIdx.y;
   const int rshift = dst.hd == 128 ? 3 : 2;
   const int slot0 = blockIdx.x << dst.tshift;
   griddep_wait();
   const int page = dst.btab[slot0 / kPage];
   const int t = threadIdx.x >> rshift;
   const bool used = slot0 + t < keep;
-  float x[16];
-  float amax = 0.f, odd = 0.f;
+  float x[2][16];
+  float amax[2] = {0.f, 0.f}, odd = 0.f;
   if (used) {
     const int slot = __ldg(index + (size_t)h * keep + slot0 + t);
     const int p = __ldg(src.btab + slot / kPage), in_page = slot % kPage;
+    uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    float s[2] = {0.f, 0.f};
     if (src.page_ok(p)) {
-      const uint8_t* codes = (which ? src.v : src.k) + src.page_row(p, h) + (size_t)in_page * src.hd;
-      const float s = __ldg((which ? src.vs : src.ks) + src.scale_at(p, h, in_page));
-      decode16(__ldg(reinterpret_cast<const uint4*>(codes + (threadIdx.x - (t << rshift)) * 16)), s, src.code, x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = 0.f;
+      const size_t at = src.page_row(p, h) + (size_t)in_page * src.hd + (threadIdx.x - (t << rshift)) * 16;
+      const size_t sc = src.scale_at(p, h, in_page);
+      u[0] = __ldg(reinterpret_cast<const uint4*>(src.k + at));
+      u[1] = __ldg(reinterpret_cast<const uint4*>(src.v + at));
+      s[0] = __ldg(src.ks + sc);
+      s[1] = __ldg(src.vs + sc);
     }
-    amax16(x, amax, odd);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      decode16(u[w], s[w], CODE, x[w]);
+      if (CODE == KV8_INT8) {  // int8 codes are numbers: a value is odd only where its scale is, or its product
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax[w] = fmaxf(amax[w], fabsf(x[w][i]));
+        odd += 0.f * s[w] + 0.f * amax[w];
+      } else {
+        amax16(x[w], amax[w], odd);
+      }
+    }
   }
   if (!dst.page_ok(page)) return;
-  const bool any_odd = __syncthreads_or(odd != odd);
-  if (any_odd) amax = used ? finite_amax16(x, 0.f) : 0.f;
-  amax = block_max(amax, red);
-  const float s = block_scale(amax, dst.code), m = inverse_scale(s);
-  uint8_t* to = (which ? dst.v : dst.k) + dst.page_row(page, h) + (size_t)(slot0 % kPage) * dst.hd + threadIdx.x * 16;
-  if (used) *reinterpret_cast<uint4*>(to) = any_odd ? encode16<true>(x, m, dst.code) : encode16<false>(x, m, dst.code);
-  if (threadIdx.x == 0) (which ? dst.vs : dst.ks)[dst.scale_at(page, h, slot0 % kPage)] = s;
+  const size_t at = dst.page_row(page, h) + (size_t)(slot0 % kPage) * dst.hd + threadIdx.x * 16;
+  const size_t sc = dst.scale_at(page, h, slot0 % kPage);
+  const float least[2] = {0.f, 0.f};
+  quantise(x, amax, odd, used, used, least, dst.code, {dst.k + at, dst.v + at}, {dst.ks + sc, dst.vs + sc}, red);
 }
 
 }  // namespace
 
 bool launch_kv8_append(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st) {
   const int t0 = a.first >> c.tshift, t1 = (a.first + a.rows - 1) >> c.tshift;
-  const dim3 grid(t1 - t0 + 1, c.n_kv, 2);
+  const dim3 grid(t1 - t0 + 1, c.n_kv);
   const int threads = (c.hd / 16) << c.tshift;
   if (io == 0)
     k_kv8_append<__nv_bfloat16><<<grid, threads, 0, st>>>(c, a);
@@ -382,13 +418,16 @@ bool launch_kv8_append(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStrea
 bool launch_kv8_read(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st) {
   const int per_slot = c.n_kv * c.hd / (io == 2 ? 4 : 8);
   const int threads = per_slot < 256 ? (per_slot + 31) / 32 * 32 : 256;
-  const dim3 grid(((a.first + a.rows - 1) >> 4) - (a.first >> 4) + 1, 2);
+  const int parts = (per_slot + threads - 1) / threads;
+  int run = 16;  // shorter runs where sixteen would leave an SM without eight CTAs
+  while (run > 1 && (long long)a.rows / run * 2 * parts < 8 * 152) run /= 2;
+  const dim3 grid((a.first + a.rows - 1) / run - a.first / run + 1, 2, parts);
   if (io == 0)
-    k_kv8_read<__nv_bfloat16><<<grid, threads, 0, st>>>(c, a);
+    k_kv8_read<__nv_bfloat16><<<grid, threads, 0, st>>>(c, a, run);
   else if (io == 1)
-    k_kv8_read<__half><<<grid, threads, 0, st>>>(c, a);
+    k_kv8_read<__half><<<grid, threads, 0, st>>>(c, a, run);
   else
-    k_kv8_read<float><<<grid, threads, 0, st>>>(c, a);
+    k_kv8_read<float><<<grid, threads, 0, st>>>(c, a, run);
   return cudaGetLastError() == cudaSuccess;
 }
 
@@ -411,9 +450,10 @@ bool launch_kv8_evict(const Kv8View& src, const Kv8View& dst, const Kv8SelectArg
   if (cudaLaunchKernelEx(&cfg, reload ? k_kv8_select<true> : k_kv8_select<false>, a) != cudaSuccess) return false;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(((a.keep - 1) >> dst.tshift) + 1, src.n_kv, 2);
+  cfg.gridDim = dim3(((a.keep - 1) >> dst.tshift) + 1, src.n_kv);
   cfg.blockDim = dim3((dst.hd / 16) << dst.tshift);
-  return cudaLaunchKernelEx(&cfg, k_kv8_gather, src, dst, (const int*)a.index, a.keep) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, src.code == KV8_INT8 ? k_kv8_gather<KV8_INT8> : k_kv8_gather<KV8_E4M3>, src, dst,
+                            (const int*)a.index, a.keep) == cudaSuccess;
 }
 
 }  // namespace ssd

@@ -138,12 +138,6 @@ __device__ __forceinline__ void scores(float (&s)[2][QT][4], const uint4 (&klo)[
                                        const uint32_t* qhi, const uint32_t* qlo, int lane) {
   constexpr int QW = HD / 16 * 64;  // words of one eight-query operand
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
-#pragma unroll
-    for (int t = 0; t < QT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[b][t][e] = 0.f;
-#pragma unroll
   for (int p = 0; p < HD / 32; ++p) {  // pairs of k steps
     uint32_t a[2][2][4];               // [step of the pair][half]
 #pragma unroll
@@ -158,7 +152,10 @@ __device__ __forceinline__ void scores(float (&s)[2][QT][4], const uint4 (&klo)[
       const uint4 h = *reinterpret_cast<const uint4*>(qhi + t * QW + (p * 32 + lane) * 4);
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        mma16816(s[b][t], a[0][b], h.x, h.y);
+        if (p == 0)
+          mma16816_first(s[b][t], a[0][b], h.x, h.y);
+        else
+          mma16816(s[b][t], a[0][b], h.x, h.y);
         mma16816(s[b][t], a[1][b], h.z, h.w);
       }
       if (SPLIT) {
@@ -675,7 +672,7 @@ constexpr int kWEights = 8;  // eights of queries staged at once
 // Grid (CTAs, KV heads).  The CTA stages up to 64 chosen queries, then its warps walk over their sixteen-slot tiles:
 // a tile's K is converted once, in registers, while the next tile's is on its way, and multiplied by every eight.
 // More queries go round again (their K comes from L2); a slot's sum stays with one lane pair throughout.
-template <typename T, int HD, int CODE>
+template <typename T, int HD, int CODE, bool CAP>
 __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_constant__ Kv8AttnArgs a, int n_slots) {
   constexpr bool SPLIT = sizeof(T) == 4;
   constexpr int NJ = HD / 64, STEPS = HD / 16;
@@ -683,11 +680,10 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
   extern __shared__ __align__(16) uint32_t smem[];
   uint32_t* s_hi = smem;
   uint32_t* s_lo = smem + kWEights * QW;
-  __shared__ float s_coef[kWEights * 8], s_lse[kWEights * 8];
+  __shared__ __align__(8) float s_coef[kWEights * 8], s_lse[kWEights * 8];
   __shared__ unsigned long long s_mask[kWEights * 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int h = blockIdx.y;
-  const bool cap = a.cap > 0.f;
   const int n_tiles = (n_slots + 15) >> 4, stride = gridDim.x * kWWarps;
   const int first = blockIdx.x * kWWarps + warp;
   const int nq = a.n_take * a.group;
@@ -718,9 +714,10 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
 
   for (int q0 = 0; q0 == 0 || q0 < nq; q0 += kWEights * 8) {
     const int eights = nq ? min(kWEights, (nq - q0 + 7) / 8) : 0;
-    Tile cur;
+    Tile cur, next;  // two tiles' codes are on their way while one is worked on
     load(cur, first, page_of(first));
-    int page = page_of(first + stride);
+    load(next, first + stride, page_of(first + stride));
+    int page = page_of(first + 2 * stride);
     if (q0) __syncthreads();
 #pragma unroll 4
     for (int q = warp; q < eights * 8; q += kWWarps) {
@@ -736,7 +733,7 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
       }
       const float inv = stage_query<T, HD, SPLIT>(p, s_hi + (q >> 3) * QW, s_lo + (q >> 3) * QW, q & 7, lane);
       if (lane == 0) {
-        s_coef[q] = qi < nq ? a.scale * inv * (cap ? 1.f : kLog2e) : 0.f;
+        s_coef[q] = qi < nq ? a.scale * inv * (CAP ? 1.f : kLog2e) : 0.f;
         // a padding query, and a row that saw nothing (lse -inf), adds exp2(-inf) = 0
         s_lse[q] = qi < nq && lse != -INFINITY ? lse * kLog2e : INFINITY;
         s_mask[q] = mask;
@@ -757,35 +754,59 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
           codes_to_half<CODE>(word_of(cur.hi[i >> 2], i & 3), k[i][1], k[i][3]);
         }
       }
-      load(cur, ti + stride, page);
-      page = page_of(ti + 2 * stride);
-      if (live) {
-        const bool full = slot0 + 16 <= a.prefix;
+      cur = next;
+      load(next, ti + 2 * stride, page);
+      page = page_of(ti + 3 * stride);
+      const int slot = slot0 + g + c * 8;  // of lanes c = 0 and 1
+      const size_t at = (size_t)h * a.ld_w + slot;
+      const bool mine = c < 2 && slot < n_slots;
+      const float before = !mine ? 0.f : q0 ? a.w_out[at] : a.w_in ? a.w_in[at] : 0.f;
+      // Scores of the tile and eight t, in the log2 domain and less the rows' log-sum-exp.
+      auto weigh = [&](int t, float (&x)[4]) {
+        float s0[4], s1[4];
+#pragma unroll
+        for (int p = 0; p < STEPS / 2; ++p) {
+          const uint4 hi = *reinterpret_cast<const uint4*>(s_hi + t * QW + (p * 32 + lane) * 4);
+          if (p == 0) {
+            mma16816_first(s0, k[0], hi.x, hi.y);
+            mma16816_first(s1, k[1], hi.z, hi.w);
+          } else {
+            mma16816(s0, k[2 * p], hi.x, hi.y);
+            mma16816(s1, k[2 * p + 1], hi.z, hi.w);
+          }
+          if (SPLIT) {
+            const uint4 lo = *reinterpret_cast<const uint4*>(s_lo + t * QW + (p * 32 + lane) * 4);
+            mma16816(s0, k[2 * p], lo.x, lo.y);
+            mma16816(s1, k[2 * p + 1], lo.z, lo.w);
+          }
+        }
+        const float2 cf = *reinterpret_cast<const float2*>(s_coef + t * 8 + 2 * c);
+        const float2 lse = *reinterpret_cast<const float2*>(s_lse + t * 8 + 2 * c);
+        const float c0 = cf.x * ks, c1 = cf.y * ks;
+        if (CAP) {
+          x[0] = capped((s0[0] + s1[0]) * c0, a.cap) - lse.x, x[1] = capped((s0[1] + s1[1]) * c1, a.cap) - lse.y;
+          x[2] = capped((s0[2] + s1[2]) * c0, a.cap) - lse.x, x[3] = capped((s0[3] + s1[3]) * c1, a.cap) - lse.y;
+        } else {
+          x[0] = fmaf(s0[0] + s1[0], c0, -lse.x), x[1] = fmaf(s0[1] + s1[1], c1, -lse.y);
+          x[2] = fmaf(s0[2] + s1[2], c0, -lse.x), x[3] = fmaf(s0[3] + s1[3], c1, -lse.y);
+        }
+      };
+      if (live && slot0 + 16 <= a.prefix) {
+#pragma unroll 2
         for (int t = 0; t < eights; ++t) {
-          float s[2][4] = {};
+          float x[4];
+          weigh(t, x);
+          sum[0] += exp2_approx(x[0]) + exp2_approx(x[1]);
+          sum[1] += exp2_approx(x[2]) + exp2_approx(x[3]);
+        }
+      } else if (live) {
+        for (int t = 0; t < eights; ++t) {
+          float x[4];
+          weigh(t, x);
 #pragma unroll
-          for (int p = 0; p < STEPS / 2; ++p) {
-            const uint4 hi = *reinterpret_cast<const uint4*>(s_hi + t * QW + (p * 32 + lane) * 4);
-            mma16816(s[0], k[2 * p], hi.x, hi.y);
-            mma16816(s[SPLIT ? 0 : 1], k[2 * p + 1], hi.z, hi.w);
-            if (SPLIT) {
-              const uint4 lo = *reinterpret_cast<const uint4*>(s_lo + t * QW + (p * 32 + lane) * 4);
-              mma16816(s[1], k[2 * p], lo.x, lo.y);
-              mma16816(s[1], k[2 * p + 1], lo.z, lo.w);
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int q = t * 8 + 2 * c + u;
-            const float cf = s_coef[q] * ks, lse = s_lse[q];
-            const unsigned long long mask = full ? 0ull : s_mask[q];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float y = s[0][2 * r + u] + s[1][2 * r + u];
-              const float x = cap ? capped(y * cf, a.cap) - lse : fmaf(y, cf, -lse);
-              sum[r] += full || visible(slot0 + g + r * 8, a.prefix, a.base, mask) ? exp2_approx(x) : 0.f;
-            }
-          }
+          for (int e = 0; e < 4; ++e)
+            if (visible(slot0 + g + (e >> 1) * 8, a.prefix, a.base, s_mask[t * 8 + 2 * c + (e & 1)]))
+              sum[e >> 1] += exp2_approx(x[e]);
         }
       }
 #pragma unroll
@@ -793,11 +814,7 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
         sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
         sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
       }
-      const int slot = slot0 + g + c * 8;
-      if (c < 2 && slot < n_slots) {
-        const size_t at = (size_t)h * a.ld_w + slot;
-        a.w_out[at] = (q0 ? a.w_out[at] : a.w_in ? a.w_in[at] : 0.f) + (c ? sum[1] : sum[0]);
-      }
+      if (mine) a.w_out[at] = before + (c ? sum[1] : sum[0]);
     }
   }
 }
@@ -856,7 +873,11 @@ bool run_weights(const Kv8AttnArgs& a, cudaStream_t st) {
   const int groups = ((n_slots + 15) / 16 + kWWarps - 1) / kWWarps;  // CTAs with a tile for every warp
   int fit = 2 * 152 / a.c.n_kv;                                       // two CTAs on each of 152 SMs
   if (fit < 1) fit = 1;
-  k_kv8_weights<T, HD, CODE><<<dim3(groups < fit ? groups : fit, a.c.n_kv), kWWarps * 32, smem, st>>>(a, n_slots);
+  const dim3 grid(groups < fit ? groups : fit, a.c.n_kv);
+  if (a.cap > 0.f)
+    k_kv8_weights<T, HD, CODE, true><<<grid, kWWarps * 32, smem, st>>>(a, n_slots);
+  else
+    k_kv8_weights<T, HD, CODE, false><<<grid, kWWarps * 32, smem, st>>>(a, n_slots);
   return cudaGetLastError() == cudaSuccess;
 }
 

@@ -44,6 +44,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same with nothing in D before.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Transpose of an 8x8 matrix of 16-bit values held one row pair per lane.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -85,7 +92,7 @@ __device__ __forceinline__ void pair_to_half(uint32_t a, uint32_t b, uint32_t (&
   codes_to_half<CODE>(z23, h[2], h[3]);
 }
 
-// Values of the four codes of a word under scale s (fp32 products; |code| <= 448 is exact in fp16 and fp32).
+// Values of the four codes of a word under scale s (fp32 products of numbers that are exact in fp16).
 __device__ __forceinline__ void decode4(uint32_t w, float s, int code, float* x) {
   uint32_t h01, h23;
   if (code == KV8_INT8)
