@@ -21,9 +21,8 @@
 // rows and the KV head's queries to an accumulator: each sixteen-slot tile is
 // one warp's, so nothing is shared and the sums have one order.
 #include <cooperative_groups.h>
-#include <math.h>
 
-#include "kv8.h"
+#include "kv8_attn.cuh"
 
 namespace ssd {
 
@@ -32,63 +31,10 @@ namespace {
 constexpr int kTileSlots = 32;   // slots that a warp takes at a time, all in one page
 constexpr int kMaxCluster = 8;   // key splits that merge in distributed shared memory
 constexpr int kMaxSplits = 152;  // key splits that merge through global memory
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kPShift = 14.f;  // softmax weights are held times 2^14, within fp16's normal range
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack_rest2(float a, float b, uint32_t hi) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  return pack_half2(a - f.x, b - f.y);
-}
-
-// Tiles of 2^SHIFT slots: those of the prefix, then those that hold new slots past them.
-template <int SHIFT>
-struct Tiles {
-  int n_prefix, first_new, n;
-  __host__ __device__ __forceinline__ Tiles(int prefix, int base, int rows) {
-    constexpr int up = (1 << SHIFT) - 1;
-    n_prefix = (prefix + up) >> SHIFT;
-    first_new = base >> SHIFT;
-    if (first_new < n_prefix) first_new = n_prefix;
-    const int end = (base + rows + up) >> SHIFT;
-    n = n_prefix + (end > first_new ? end - first_new : 0);
-  }
-  __device__ __forceinline__ int slot(int t) const { return (t < n_prefix ? t : first_new + t - n_prefix) << SHIFT; }
-};
-
-__device__ __forceinline__ bool visible(int slot, int prefix, int base, unsigned long long mask) {
-  const unsigned e = (unsigned)(slot - base);
-  return slot < prefix || (e < 64u && ((mask >> e) & 1ull));
-}
-
-// Whether any row sees one of the sixteen slots from `slot` on.
-__device__ __forceinline__ bool visible_any(int slot, const Kv8AttnArgs& a) {
-  if (slot < a.prefix) return true;
-  const int e = slot - a.base;
-  if (e <= -16 || e >= 64) return false;
-  return ((e >= 0 ? a.any >> e : a.any << -e) & 0xffffull) != 0;
-}
-
 __device__ __forceinline__ uint4 ld16(const uint8_t* p) {
   uint4 r;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
-}
-
-// A pair of neighbouring query elements as fp32.
-__device__ __forceinline__ float2 load2(const float* p) { return __ldg(reinterpret_cast<const float2*>(p)); }
-__device__ __forceinline__ float2 load2(const __half* p) { return __half22float2(__ldg(reinterpret_cast<const __half2*>(p))); }
-__device__ __forceinline__ float2 load2(const __nv_bfloat16* p) {
-  return __bfloat1622float2(__ldg(reinterpret_cast<const __nv_bfloat162*>(p)));
 }
 
 // Lay out a query as column `col` of the MMA's B operand in shared memory.  Lane (g, c) of the MMA multiplies column
@@ -108,14 +54,8 @@ __device__ __forceinline__ float stage_query(const T* q, uint32_t* hi, uint32_t*
     amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
   }
   amax = warp_max(amax);
-  // a power of two that brings the largest magnitude into [128, 256)
-  int ex = (int)(__float_as_uint(amax) >> 23);
-  float f = 1.f, inv = 1.f;
-  if (amax > 0.f && ex < 255) {
-    ex = max(ex, 16);
-    f = __uint_as_float((uint32_t)(261 - ex) << 23);
-    inv = __uint_as_float((uint32_t)(ex - 7) << 23);
-  }
+  float f, inv;
+  query_factor(amax, f, inv);
 #pragma unroll
   for (int i = 0; i < EPL / 2; ++i) {
     const int e = 64 * i + 2 * lane;  // even element of the pair
@@ -170,13 +110,6 @@ __device__ __forceinline__ void scores(float (&s)[2][QT][4], const uint4 (&klo)[
   }
 }
 
-// The capped score in the log2 domain: tanh y = 1 - 2 / (1 + e^2y), whose error of a few 2^-24 is absolute, so that
-// a score is off by that many parts of the cap.
-__device__ __forceinline__ float capped(float x, float cap) {
-  const float e = exp2_approx(x * (2.f * kLog2e / cap));
-  return cap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
-}
-
 // A warp's ring of 32-slot tiles in shared memory: the K rows, then the V rows.  Sixteen-byte chunks are swizzled
 // inside 128-byte lines, so that neither a lane's chunks of its own K row nor its run of four V rows meet in a bank.
 template <int HD, int STAGES>
@@ -202,19 +135,6 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-
-// Four neighbouring values of an output row.
-template <typename T>
-__device__ __forceinline__ void store4(T* p, const float4& y) {
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = y;
-  } else {
-    __align__(8) T t[4] = {Io<T>::from_f(y.x), Io<T>::from_f(y.y), Io<T>::from_f(y.z), Io<T>::from_f(y.w)};
-    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(t);
-  }
-}
-
-__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m - kPShift + log2f(l)) * kLn2; }
 
 // Warps of a CTA and stages of a warp's ring.  Eight queries leave registers for twelve warps, which hide the
 // latency of the conversions, with two stages each (8 KB under way a warp, 96 KB an SM); the larger blocks run
@@ -842,15 +762,7 @@ bool run_attention(Kv8AttnArgs a, cudaStream_t st) {
     attr[0].val.clusterDim.z = 1;
     cfg.numAttrs = 1;
   }
-  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return false;
-  if (!a.part_o) return true;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(a.c.n_kv * nq);
-  cfg.blockDim = dim3(HD);
-  cfg.dynamicSmemBytes = 0;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_kv8_merge<T, HD>, a) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess;
 }
 
 // Query eights of a CTA: all of a KV head's queries up to four eights.
@@ -881,6 +793,21 @@ bool run_weights(const Kv8AttnArgs& a, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess;
 }
 
+// Add up the splits of scratch.
+template <typename T>
+bool run_merge(const Kv8AttnArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(a.c.n_kv * a.rows * a.group);
+  cfg.blockDim = dim3(a.c.hd);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, a.c.hd == 128 ? k_kv8_merge<T, 128> : k_kv8_merge<T, 64>, a) == cudaSuccess;
+}
+
 template <typename T>
 bool attention_of(const Kv8AttnArgs& a, cudaStream_t st) {
   const bool i8 = a.c.code == KV8_INT8;
@@ -898,22 +825,38 @@ bool weights_of(const Kv8AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-Kv8Splits kv8_attention_splits(int rows, int group, int n_kv, int slots) {
-  const int nq = rows * group, qb = 8 * query_eights(nq);
+// From this many queries of a KV head on the tensor-core kernel runs.
+constexpr int kTcQueries = 64;
+
+Kv8Splits kv8_attention_splits(int rows, int group, int n_kv, int slots, int io) {
+  const int nq = rows * group;
+  const bool tc = nq > kTcQueries;
+  const int qb = tc ? (io == 2 ? 128 : 256) : 8 * query_eights(nq);
   const int blocks = n_kv * ((nq + qb - 1) / qb);
-  const int tiles = (slots + kTileSlots - 1) / kTileSlots;
+  const int slots_a_tile = tc ? 128 : kTileSlots;
+  const int tiles = (slots + slots_a_tile - 1) / slots_a_tile;
   const int fit = kMaxSplits / blocks;                     // one CTA on each of 152 SMs
-  const int warps = qb == 8 ? 12 : 8;
-  const int most = (tiles + warps - 1) / warps;            // a tile for every warp
+  const int warps = tc ? 1 : qb == 8 ? 12 : 8;
+  const int most = (tiles + warps - 1) / warps;            // a tile for every warp (for the CTA)
   int n = fit < most ? fit : most;
-  if (n <= 1) return {1, false};
+  if (n <= 1) return {1, false, tc};
   const int per = (tiles + n - 1) / n;
   n = (tiles + per - 1) / per;                             // no split without a tile
-  return {n, n > kMaxCluster};
+  // A GPC of sixteen SMs holds fifteen or sixteen CTAs in clusters of up to five, but twelve in clusters of six; where
+  // the CTAs would fill half the chip, larger clusters run in two waves (72 queries a head over 4000 slots: 34.2 us in
+  // clusters of six, 21.5 us for 128 queries in clusters of four).
+  const bool cluster = n <= 5 || (n <= kMaxCluster && n * blocks <= 76);
+  return {n, tc || !cluster, tc};
 }
 
-bool launch_kv8_attention(const Kv8AttnArgs& a, int io, cudaStream_t st) {
-  return io == 0 ? attention_of<__nv_bfloat16>(a, st) : io == 1 ? attention_of<__half>(a, st) : attention_of<float>(a, st);
+bool launch_kv8_attention(const Kv8AttnArgs& a, int io, bool tc, cudaStream_t st) {
+  if (tc) {
+    if (!launch_kv8_attention_tc(a, io, st)) return false;
+  } else if (!(io == 0 ? attention_of<__nv_bfloat16>(a, st) : io == 1 ? attention_of<__half>(a, st) : attention_of<float>(a, st))) {
+    return false;
+  }
+  if (!a.part_o) return true;
+  return io == 0 ? run_merge<__nv_bfloat16>(a, st) : io == 1 ? run_merge<__half>(a, st) : run_merge<float>(a, st);
 }
 
 bool launch_kv8_weights(const Kv8AttnArgs& a, int io, cudaStream_t st) {

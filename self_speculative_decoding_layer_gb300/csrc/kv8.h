@@ -51,14 +51,15 @@ struct Kv8AttnArgs {
 bool launch_kv8_append(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st);
 bool launch_kv8_read(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st);
 bool launch_kv8_evict(const Kv8View& src, const Kv8View& dst, const Kv8SelectArgs& a, cudaStream_t st);
-// Key splits of an attention launch over `slots` slots, and whether they merge through device scratch (else in
-// the distributed shared memory of a cluster).
+// Key splits of an attention launch over `slots` slots, whether they merge through device scratch (else in the
+// distributed shared memory of a cluster), and whether the tensor-core kernel runs it.
 struct Kv8Splits {
   int n;
-  bool scratch;
+  bool scratch, tc;
 };
-Kv8Splits kv8_attention_splits(int rows, int group, int n_kv, int slots);
-bool launch_kv8_attention(const Kv8AttnArgs& a, int io, cudaStream_t st);
+Kv8Splits kv8_attention_splits(int rows, int group, int n_kv, int slots, int io);
+bool launch_kv8_attention(const Kv8AttnArgs& a, int io, bool tc, cudaStream_t st);
+bool launch_kv8_attention_tc(const Kv8AttnArgs& a, int io, cudaStream_t st);
 bool launch_kv8_weights(const Kv8AttnArgs& a, int io, cudaStream_t st);
 
 }  // namespace ssd

@@ -88,9 +88,10 @@ bool attn_args(const ssd_kv8_cache* c, const ssd_kv8_attention_args* p, Kv8AttnA
 int slots_of(const Kv8AttnArgs& a) { return a.prefix > a.base + a.rows ? a.prefix : a.base + a.rows; }
 
 // Sets a's key splits; bytes of scratch that they need.
-size_t split(Kv8AttnArgs* a) {
-  const Kv8Splits s = kv8_attention_splits(a->rows, a->group, a->c.n_kv, slots_of(*a));
+size_t split(Kv8AttnArgs* a, int io, bool* tc) {
+  const Kv8Splits s = kv8_attention_splits(a->rows, a->group, a->c.n_kv, slots_of(*a), io);
   a->n_split = s.n;
+  *tc = s.tc;
   return s.scratch ? (size_t)a->c.n_kv * a->rows * a->group * s.n * (a->c.hd + 2) * 4 : 0;
 }
 
@@ -113,7 +114,8 @@ ssd_status ssd_kv8_read(const ssd_kv8_cache* cache, const ssd_kv8_rows* rows, vo
 size_t ssd_kv8_attention_scratch_bytes(const ssd_kv8_cache* cache, const ssd_kv8_attention_args* args) {
   Kv8AttnArgs a{};
   if (!attn_args(cache, args, &a)) return 0;
-  const size_t b = split(&a);
+  bool tc;
+  const size_t b = split(&a, args->dtype, &tc);
   return b < 256 ? 256 : (b + 255) / 256 * 256;
 }
 
@@ -124,14 +126,15 @@ ssd_status ssd_kv8_attention(const ssd_kv8_cache* cache, const ssd_kv8_attention
   if (!rows_ok(args->out, args->ld_out, (int64_t)a.n_q * a.c.hd, args->dtype)) return SSD_ERR_INVALID_ARG;
   a.out = args->out;
   a.ld_out = (size_t)args->ld_out;
-  const size_t need = split(&a);
+  bool tc;
+  const size_t need = split(&a, args->dtype, &tc);
   if (need) {
     if (!scratch || ((uintptr_t)scratch & 255)) return SSD_ERR_INVALID_ARG;
     if (scratch_bytes < need) return SSD_ERR_CAPACITY;
     a.part_o = (float*)scratch;
     a.part_ml = (float2*)(a.part_o + (size_t)a.c.n_kv * a.rows * a.group * a.n_split * a.c.hd);
   }
-  return launch_kv8_attention(a, args->dtype, (cudaStream_t)stream) ? SSD_OK : SSD_ERR_CUDA;
+  return launch_kv8_attention(a, args->dtype, tc, (cudaStream_t)stream) ? SSD_OK : SSD_ERR_CUDA;
 }
 
 ssd_status ssd_kv8_weights(const ssd_kv8_cache* cache, const ssd_kv8_attention_args* args, uint64_t row_set,

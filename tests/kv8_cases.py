@@ -68,7 +68,8 @@ def out_error(q, k, v, vis, want, scale, cap, io):
     top = np.where(vis.any(0)[:, None, None], vv, 0.0).max((0, 2))[None, :]
     rel = 2 * (2 * e + 2.0 ** -22 * (1 + np.abs(np.where(np.isfinite(m[..., 0]), m[..., 0], 0.0)))) + (n / 16 + 200) * 2.0 ** -23
     rel = rel + (2.0 ** -21 if io == "fp32" else 2.0 ** -11)
-    floor = n * 2.0 ** -37 * top / total  # weights that end below fp16's smallest step (2^-24 under 2^14)
+    # weights that end below fp16's smallest step: 2^-24 under 2^9 (the tensor-core kernel; 2^14 elsewhere), half of it
+    floor = n * 2.0 ** -34 * top / total
     out = rel[..., None] * mean_v + floor[..., None]
     half = {"fp32": U24, "bf16": U8, "fp16": U11}[io]
     # fp16 numbers below 2^-14 lie 2^-24 apart: rounding to one is off by up to 2^-25 whatever the value (an output of
