@@ -25,7 +25,9 @@ namespace ssd {
 namespace {
 
 constexpr int kTcTile = 128;      // slots of a tile
-constexpr int kTcThreads = 416;   // warps 0-3 and 4-7: softmax of query blocks 0 and 1; 8-11 converters; 12 MMA
+constexpr int kConvWarps = 8;
+constexpr int kMmaWarp = 8 + kConvWarps;
+constexpr int kTcThreads = (kMmaWarp + 1) * 32;  // warps 0-3 and 4-7: softmax of query blocks 0 and 1; converters; MMA
 constexpr int kTcStages = 2;
 constexpr float kTcShift = 9.f;   // softmax weights are held times 2^9, and grow to 2^(9 + kSlack) < 2^16
 constexpr float kSlack = 6.f;
@@ -59,20 +61,28 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lead) {
 __device__ __forceinline__ constexpr uint32_t idesc_h(int n, bool trans_b) {
   return (1u << 4) | (trans_b ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accum) {
+// Issued by the lane that `issue` names; the whole warp executes the code around, so that descriptors stay in uniform
+// registers.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accum, uint32_t issue) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accum)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accum), "r"(issue)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accum) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accum, uint32_t issue) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accum)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accum), "r"(issue)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t issue) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)),
+      "r"(issue)
+      : "memory");
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -80,9 +90,8 @@ __device__ __forceinline__ void arrive(uint64_t* bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 32 columns of this warp's 32 TMEM lanes.
-__device__ __forceinline__ void tmem_ld32(uint32_t t, float (&f)[32]) {
-  uint32_t r[32];
+// Ask for 32 columns of this warp's 32 TMEM lanes; r holds them after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t t, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
       "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -91,9 +100,35 @@ __device__ __forceinline__ void tmem_ld32(uint32_t t, float (&f)[32]) {
         "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(t));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// Wait for every load that this thread has asked for; the operands keep r's uses behind the wait.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t t, float (&f)[32]) {
+  uint32_t r[32];
+  tmem_ld32_async(t, r);
+  tmem_wait_ld(r);
 #pragma unroll
   for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+}
+// The largest of sixteen.
+__device__ __forceinline__ float max16(const uint32_t* r) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = fmaxf(__uint_as_float(r[i]), __uint_as_float(r[i + 8]));
+#pragma unroll
+  for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) y[i] = fmaxf(y[i], y[i + n]);
+  return y[0];
 }
 __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&r)[16]) {
   asm volatile(
@@ -124,7 +159,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
   uint64_t* p_full = s_full + NQT;            // [NQT] softmax -> MMA
   uint64_t* pv_done = p_full + NQT;           // [NQT] MMA -> softmax
   __shared__ uint32_t s_tmem;
-  __shared__ float s_red[4], s_vref;
+  __shared__ float s_red[kConvWarps], s_vref;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x, h = blockIdx.y, q0 = blockIdx.z * 128 * NQT;
   const int nq = a.rows * a.group;
@@ -134,13 +169,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
   const int t_first = min(tiles.n, split * a.split_tiles), t_last = min(tiles.n, t_first + a.split_tiles);
   const int n_tile = t_last - t_first;
 
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     if (lane == 0) {
       for (int i = 0; i < kTcStages; ++i) {
-        mbar_init(&kv_full[i], 128);
+        mbar_init(&kv_full[i], kConvWarps * 32);
         mbar_init(&kv_empty[i], 1);
       }
       for (int i = 0; i < NQT; ++i) {
@@ -151,16 +186,53 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
       fence_barrier_init();
     }
   }
-  // Queries: a warp takes four at a time (all of their loads first), as fp16 rows times their power of two.
-  constexpr int QG = 4;
-  for (int g0 = warp * QG; g0 < n_act * 128; g0 += kTcThreads / 32 * QG) {
+  // Converters: thread ct takes sixteen-byte chunk ct % CH of rows ct / CH + RS i of every tile.  What they need
+  // first is asked for before the queries are staged.
+  constexpr int CH = HD / 16, RS = kConvWarps * 32 / CH, NI = 128 / RS;
+  const int ct = threadIdx.x - 256, ch = ct & (CH - 1), r0 = (ct & (kConvWarps * 32 - 1)) / CH;
+  // Page `half` of tile j; -1 where it is none or no row sees a slot of it.
+  auto page_of = [&](int j, int half) {
+    if (j >= n_tile) return -1;
+    const int slot = tiles.slot(t_first + j) + half * kPage;
+    if (!visible_any(slot, a) && !visible_any(slot + 16, a) && !visible_any(slot + 32, a) && !visible_any(slot + 48, a))
+      return -1;
+    const int page = __ldg(a.c.btab + slot / kPage);
+    return a.c.page_ok(page) ? page : -1;
+  };
+  uint4 k[NI], v[NI];
+  // Byte offset of this thread's first chunk in a page's rows of this head.
+  auto page_at = [&](int page) { return page < 0 ? (size_t)0 : a.c.page_row(page, h) + (size_t)r0 * HD + ch * 16; };
+  auto load = [&](int i, int j, int page, size_t at, bool whole) {  // chunk i of tile j: row r0 + RS i
+    // (rows that hold no token may hold any bits)
+    if (page >= 0 && (whole || visible(tiles.slot(t_first + j) + r0 + RS * i, a.prefix, a.base, a.any))) {
+      const size_t o = at + (RS * i % kPage) * HD;
+      k[i] = __ldg(reinterpret_cast<const uint4*>(a.c.k + o));
+      v[i] = __ldg(reinterpret_cast<const uint4*>(a.c.v + o));
+    } else {
+      k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  auto whole_of = [&](int j) { return tiles.slot(t_first + j) + kTcTile <= a.prefix; };
+  const bool converter = warp >= 8 && warp < kMmaWarp;
+  int p0 = -1, p1 = -1;
+  if (converter && n_tile > 0) {
+    p0 = page_of(0, 0);
+    p1 = page_of(0, 1);
+    const size_t a0 = page_at(p0), a1 = page_at(p1);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) load(i, 0, RS * i < kPage ? p0 : p1, RS * i < kPage ? a0 : a1, whole_of(0));
+  }
+  // Queries: a warp takes eight at a time (all of their loads first), as fp16 rows times their power of two.
+  constexpr int QG = 8;
+  for (int g0 = (warp < 8 ? warp : 8) * QG; !converter && g0 < n_act * 128; g0 += 9 * QG) {
     float2 x[QG][HB];
+    int r = (q0 + g0) / a.group, e = q0 + g0 - r * a.group;
 #pragma unroll
     for (int u = 0; u < QG; ++u) {
-      const int qi = q0 + g0 + u, r = qi / a.group;
-      const T* p = reinterpret_cast<const T*>(a.q) + (size_t)r * a.ld_q + (size_t)(h * a.group + qi - r * a.group) * HD;
+      const T* p = reinterpret_cast<const T*>(a.q) + (size_t)r * a.ld_q + (size_t)(h * a.group + e) * HD;
 #pragma unroll
-      for (int b = 0; b < HB; ++b) x[u][b] = qi < nq ? load2(p + b * 64 + 2 * lane) : make_float2(0.f, 0.f);
+      for (int b = 0; b < HB; ++b) x[u][b] = r < a.rows ? load2(p + b * 64 + 2 * lane) : make_float2(0.f, 0.f);
+      if (++e == a.group) e = 0, ++r;
     }
 #pragma unroll
     for (int u = 0; u < QG; ++u) {
@@ -169,7 +241,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
 #pragma unroll
       for (int b = 0; b < HB; ++b) amax = fmaxf(amax, fmaxf(fabsf(x[u][b].x), fabsf(x[u][b].y)));
       float f, inv;
-      query_factor(warp_max(amax), f, inv);
+      query_factor(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))), f, inv);  // (amax >= 0)
       unsigned char* to = s_q + (q >> 7) * (SPLIT ? 2 : 1) * L::kMat + row * 128 +
                           ((((lane >> 2) ^ (row & 7)) << 4) | ((lane & 3) << 2));
 #pragma unroll
@@ -190,48 +262,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
   // TMEM columns: S of block qt (P hi over its first half); P lo (SPLIT, one block); O of block qt
   const uint32_t c_lo = 128, c_o = 256;
 
-  if (warp >= 8 && warp < 12) {
-    // ---- converters: thread ct takes sixteen-byte chunk ct % CH of rows ct / CH + 16 i (HD 128) or 32 i (HD 64)
-    constexpr int CH = HD / 16, RS = 128 / CH, NI = 128 / RS;
-    const int ct = threadIdx.x - 256, ch = ct % CH, r0 = ct / CH;
+  if (converter) {
+    // ---- converters
     float vmax = 0.f;  // V's largest scale in the split
-    for (int i = ct; i < n_tile * 8; i += 128) {
+    for (int i = ct; i < n_tile * 8; i += kConvWarps * 32) {
       const int slot = tiles.slot(t_first + (i >> 3)) + (i & 7) * 16;
       if (!visible_any(slot, a)) continue;
       const int page = __ldg(a.c.btab + slot / kPage);
       if (a.c.page_ok(page)) vmax = fmaxf(vmax, __ldg(a.c.vs + a.c.scale_at(page, h, slot % kPage)));
     }
     vmax = warp_max(vmax);
-    if (lane == 0) s_red[warp & 3] = vmax;
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-    vmax = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+    if (lane == 0) s_red[warp - 8] = vmax;
+    asm volatile("bar.sync 1, %0;" ::"n"(kConvWarps * 32) : "memory");
+    vmax = warp_max(s_red[lane % kConvWarps]);
     const float vref = vmax > 0.f ? vmax : 1.f;
     if (ct == 0) s_vref = vref;
 
-    // Page `half` of tile j; -1 where it is none or no row sees a slot of it.
-    auto page_of = [&](int j, int half) {
-      if (j >= n_tile) return -1;
-      const int slot = tiles.slot(t_first + j) + half * kPage;
-      if (!visible_any(slot, a) && !visible_any(slot + 16, a) && !visible_any(slot + 32, a) && !visible_any(slot + 48, a))
-        return -1;
-      const int page = __ldg(a.c.btab + slot / kPage);
-      return a.c.page_ok(page) ? page : -1;
-    };
-    uint4 k[NI], v[NI];
-    auto load = [&](int i, int j, int page) {  // chunk i of tile j: row r0 + RS i
-      const int row = r0 + RS * i, slot = tiles.slot(t_first + j) + row;
-      k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (page >= 0 && visible(slot, a.prefix, a.base, a.any)) {  // (rows that hold no token may hold any bits)
-        const size_t at = a.c.page_row(page, h) + (size_t)(row % kPage) * HD + ch * 16;
-        k[i] = __ldg(reinterpret_cast<const uint4*>(a.c.k + at));
-        v[i] = __ldg(reinterpret_cast<const uint4*>(a.c.v + at));
-      }
-    };
-    int p0 = page_of(0, 0), p1 = page_of(0, 1);
-    if (n_tile > 0) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) load(i, 0, RS * i < kPage ? p0 : p1);
-    }
     int n0 = page_of(1, 0), n1 = page_of(1, 1);
     for (int j = 0; j < n_tile; ++j) {
       const int st = j & 1;
@@ -246,25 +292,38 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
         }
       }
       if (j >= kTcStages && !mbar_wait_bounded(&kv_empty[st], (uint32_t)((j >> 1) - 1) & 1u)) break;
-      unsigned char* dst = s_kv + st * L::kStage + (ch >> 2) * BLK;
+      unsigned char* dst = s_kv + st * L::kStage + (ch >> 2) * BLK + r0 * 128;
+      const size_t a0 = page_at(n0), a1 = page_at(n1);
+      const bool more = j + 1 < n_tile, whole = more && whole_of(j + 1);
+      // Chunk i becomes two sixteen-byte chunks of fp16 for K and for V, stored in an order that alternates with the
+      // 64-wide block, so that a row's lanes meet in no bank.  (r0 + RS i and r0 have the same three low bits.)
+      const int flip = ch >> 2, c0 = (ch & 3) * 2;
+      const uint32_t t0 = (uint32_t)((c0 + flip) ^ (r0 & 7)) << 4, t1 = (uint32_t)((c0 + 1 - flip) ^ (r0 & 7)) << 4;
+      auto convert = [&](const uint4& u, unsigned char* to) {
+        uint4 w0, w1;
+        codes_to_half<CODE>(flip ? u.z : u.x, w0.x, w0.y);
+        codes_to_half<CODE>(flip ? u.w : u.y, w0.z, w0.w);
+        codes_to_half<CODE>(flip ? u.x : u.z, w1.x, w1.y);
+        codes_to_half<CODE>(flip ? u.y : u.w, w1.z, w1.w);
+        *reinterpret_cast<uint4*>(to + t0) = w0;
+        *reinterpret_cast<uint4*>(to + t1) = w1;
+      };
+      if (whole && n0 >= 0 && n1 >= 0) {
+        const uint8_t *k0 = a.c.k + a0, *k1 = a.c.k + a1, *v0 = a.c.v + a0, *v1 = a.c.v + a1;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int row = r0 + RS * i;
-        unsigned char* to = dst + row * 128;
-        // two sixteen-byte chunks of fp16; the order alternates so that a row's lanes meet in no bank
-        const int c0 = (ch & 3) * 2, flip = ch >> 2;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const uint4 u = m ? v[i] : k[i];
-          uint4 w[2];
-          codes_to_half<CODE>(u.x, w[0].x, w[0].y);
-          codes_to_half<CODE>(u.y, w[0].z, w[0].w);
-          codes_to_half<CODE>(u.z, w[1].x, w[1].y);
-          codes_to_half<CODE>(u.w, w[1].z, w[1].w);
-          *reinterpret_cast<uint4*>(to + m * L::kMat + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? w[1] : w[0];
-          *reinterpret_cast<uint4*>(to + m * L::kMat + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? w[0] : w[1];
+        for (int i = 0; i < NI; ++i) {
+          convert(k[i], dst + i * RS * 128);
+          convert(v[i], dst + i * RS * 128 + L::kMat);
+          k[i] = __ldg(reinterpret_cast<const uint4*>((RS * i < kPage ? k0 : k1) + (RS * i % kPage) * HD));
+          v[i] = __ldg(reinterpret_cast<const uint4*>((RS * i < kPage ? v0 : v1) + (RS * i % kPage) * HD));
         }
-        if (j + 1 < n_tile) load(i, j + 1, RS * i < kPage ? n0 : n1);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          convert(k[i], dst + i * RS * 128);
+          convert(v[i], dst + i * RS * 128 + L::kMat);
+          if (more) load(i, j + 1, RS * i < kPage ? n0 : n1, RS * i < kPage ? a0 : a1, whole);
+        }
       }
       if (ct < 8) {
         const float r = vs / vref;
@@ -283,45 +342,48 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
       n0 = page_of(j + 2, 0);
       n1 = page_of(j + 2, 1);
     }
-  } else if (warp == 12) {
-    if (lane == 0 && n_tile > 0) {
+  } else if (warp == kMmaWarp) {
+    if (n_tile > 0) {
       // ---- MMA issuer
-      const uint32_t kv0 = smem_u32(s_kv), qb = smem_u32(s_q);
+      const uint32_t issue = lane == 0;
       constexpr uint32_t id_s = idesc_h(kTcTile, false), id_o = idesc_h(HD, true);
+      const uint64_t dq = desc_k(smem_u32(s_q)), dk = desc_k(smem_u32(s_kv));
+      const uint64_t dv = desc_mn(smem_u32(s_kv) + L::kMat, BLK);
+      // (descriptors count addresses in sixteen bytes; all of shared memory fits their field)
       auto qk = [&](int qt, int st) {
-        const uint32_t q = qb + qt * (SPLIT ? 2 : 1) * L::kMat, k = kv0 + st * L::kStage;
+        const uint64_t q = dq + (uint32_t)(qt * (SPLIT ? 2 : 1) * L::kMat >> 4), k = dk + (uint32_t)(st * L::kStage >> 4);
 #pragma unroll
         for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
             const uint32_t off = (kk >> 2) * BLK + (kk & 3) * 32;
-            mma_ss(tmem + qt * 128, desc_k(q + part * L::kMat + off), desc_k(k + off), id_s, part > 0 || kk > 0);
+            mma_ss(tmem + qt * 128, q + ((part * L::kMat + off) >> 4), k + (off >> 4), id_s, part > 0 || kk > 0, issue);
           }
-        commit(&s_full[qt]);
+        commit(&s_full[qt], issue);
       };
       auto pv = [&](int qt, int st, bool first) {
-        const uint32_t v = kv0 + st * L::kStage + L::kMat;
+        const uint64_t v = dv + (uint32_t)(st * L::kStage >> 4);
 #pragma unroll
         for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
 #pragma unroll
           for (int kk = 0; kk < kTcTile / 16; ++kk)
-            mma_ts(tmem + c_o + qt * 128, tmem + (part ? c_lo : qt * 128) + kk * 8, desc_mn(v + kk * 2048, BLK), id_o,
-                   !(first && part == 0 && kk == 0));
-        commit(&pv_done[qt]);
+            mma_ts(tmem + c_o + qt * 128, tmem + (part ? c_lo : qt * 128) + kk * 8, v + kk * (2048 >> 4), id_o,
+                   !(first && part == 0 && kk == 0), issue);
+        commit(&pv_done[qt], issue);
       };
-      bool ok = mbar_wait_bounded(&kv_full[0], 0u);
+      bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&kv_full[0], 0u));
       fence_after();
       for (int qt = 0; ok && qt < n_act; ++qt) qk(qt, 0);
       for (int j = 0; ok && j < n_tile; ++j) {
         for (int qt = 0; qt < n_act; ++qt) {
-          ok = mbar_wait_bounded(&p_full[qt], (uint32_t)j & 1u);
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&p_full[qt], (uint32_t)j & 1u));
           if (!ok) break;
           fence_after();
           pv(qt, j & 1, j == 0);
-          if (qt == n_act - 1) commit(&kv_empty[j & 1]);
+          if (qt == n_act - 1) commit(&kv_empty[j & 1], issue);
           if (j + 1 < n_tile) {
             if (qt == 0) {
-              ok = mbar_wait_bounded(&kv_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u);
+              ok = __all_sync(0xffffffffu, mbar_wait_bounded(&kv_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u));
               if (!ok) break;
               fence_after();
             }
@@ -365,20 +427,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
           x[i] = (b >> i) & 1u ? (cap ? capped(y, a.cap) : y) : -INFINITY;
         }
       };
+      // A plain tile's columns are asked for a chunk ahead; the others' loops stay rolled, so that the code fits the
+      // instruction cache.
       float top = -INFINITY;
-#pragma unroll 1  // (unrolled, the loops' code no longer fits the instruction cache)
-      for (int c = 0; c < 4; ++c) {
-        float x[32];
-        tmem_ld32(ts + c * 32, x);
-        if (full) {
+      if (full) {
+        uint32_t x[2][32];
+        tmem_ld32_async(ts, x[0]);
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            float y = x[b * 16];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) y = fmaxf(y, x[b * 16 + i]);
-            top = fmaxf(top, y * (coef * hd.ks[2 * c + b]));
-          }
-        } else {
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld(x[c & 1]);
+          if (c < 3) tmem_ld32_async(ts + (c + 1) * 32, x[(c + 1) & 1]);
+          top = fmaxf(top, fmaxf(max16(x[c & 1]) * (coef * hd.ks[2 * c]), max16(x[c & 1] + 16) * (coef * hd.ks[2 * c + 1])));
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float x[32];
+          tmem_ld32(ts + c * 32, x);
           slow(x, c);
 #pragma unroll
           for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i]);
@@ -406,27 +471,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
         }
       }
       const float ref = kTcShift - (m == -INFINITY ? 0.f : m);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        float x[32];
-        tmem_ld32(ts + c * 32, x);
-        if (!full) slow(x, c);
+      // Weights of 32 columns whose scores (times cf0 / cf1) are x: into P, over columns that have been read already.
+      auto weigh = [&](const uint32_t (&x)[32], int c, float cf0, float cf1) {
         uint32_t hi[16], lo[16];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const float cf = full ? coef * hd.ks[2 * c + b] : 1.f, add = ref + hd.lrv[2 * c + b];
-          float sum = 0.f;
+          const float cf = b ? cf1 : cf0, add = ref + hd.lrv[2 * c + b];
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float p0 = exp2_approx(fmaf(x[b * 16 + i], cf, add)), p1 = exp2_approx(fmaf(x[b * 16 + i + 1], cf, add));
-            sum += p0 + p1;
+            const float p0 = exp2_approx(fmaf(__uint_as_float(x[b * 16 + i]), cf, add));
+            const float p1 = exp2_approx(fmaf(__uint_as_float(x[b * 16 + i + 1]), cf, add));
+            sum[(i & 2)] += p0;
+            sum[(i & 2) + 1] += p1;
             hi[b * 8 + i / 2] = pack_half2(p0, p1);
             if (SPLIT) lo[b * 8 + i / 2] = pack_rest2(p0, p1, hi[b * 8 + i / 2]);
           }
-          l = fmaf(sum, hd.irv[2 * c + b], l);
+          l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), hd.irv[2 * c + b], l);
         }
-        tmem_st16(ts + c * 16, hi);  // columns that have been read already
+        tmem_st16(ts + c * 16, hi);
         if (SPLIT) tmem_st16(tl + c * 16, lo);
+      };
+      if (full) {
+        uint32_t x[2][32];
+        tmem_ld32_async(ts, x[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait_ld(x[c & 1]);
+          if (c < 3) tmem_ld32_async(ts + (c + 1) * 32, x[(c + 1) & 1]);
+          weigh(x[c & 1], c, coef * hd.ks[2 * c], coef * hd.ks[2 * c + 1]);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float x[32];
+          uint32_t y[32];
+          tmem_ld32(ts + c * 32, x);
+          slow(x, c);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(x[i]);
+          weigh(y, c, 1.f, 1.f);
+        }
       }
       tmem_wait_st();
       fence_before();
@@ -472,7 +557,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
   __syncwarp();
   fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
