@@ -76,7 +76,8 @@ class Cache8:
 def scores(q, k, scale, cap):
     """[R, Hq, n] scores of q [R, Hq, hd] against k [n, H, hd] in float64."""
     group = q.shape[1] // k.shape[1]
-    s = np.einsum("rhd,nhd->rhn", q.astype(np.float64), np.repeat(k.astype(np.float64), group, 1)) * scale
+    keys = np.repeat(k.astype(np.float64), group, 1).transpose(1, 2, 0)  # [Hq, hd, n]
+    s = np.matmul(q.astype(np.float64).transpose(1, 0, 2), keys).transpose(1, 0, 2) * scale
     return cap * np.tanh(s / cap) if cap else s
 
 
@@ -89,7 +90,8 @@ def attention(q, k, v, vis, scale=None, cap=0.0):
     p = np.exp(s - np.where(np.isfinite(m), m, 0.0))
     total = p.sum(-1, keepdims=True)
     v = np.where(vis.any(0)[:, None, None], v.astype(np.float64), 0.0)
-    o = np.einsum("rhn,nhd->rhd", p / np.where(total > 0, total, 1.0), np.repeat(v, group, 1))
+    p = p / np.where(total > 0, total, 1.0)
+    o = np.matmul(p.transpose(1, 0, 2), np.repeat(v, group, 1).transpose(1, 0, 2)).transpose(1, 0, 2)
     with np.errstate(divide="ignore"):
         return o, (np.where(np.isfinite(m), m, 0.0) + np.log(total))[..., 0]
 

@@ -825,12 +825,15 @@ bool weights_of(const Kv8AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// From this many queries of a KV head on the tensor-core kernel runs.
-constexpr int kTcQueries = 64;
+// The tcgen05 kernel runs where a KV head has more than 32 queries and the 32-query blocks times the slots of all heads
+// reach this many (64 rows of 64 query heads on 8, bf16: over 1500 slots, 192000 of these units, it takes 31.0 us and the
+// other 26.7; over 4000 33.3 and 49.3; over 16000 61.0 and 156.  64 queries a head: over 16000, 256000 units, 29.5 and
+// 30.2.  64 rows of 40 heads: over 1500, 120000 units, 26.5 and 26.7, over 4000 35.8 and 51.1).
+constexpr long long kTcWork = 200000;
 
 Kv8Splits kv8_attention_splits(int rows, int group, int n_kv, int slots, int io) {
   const int nq = rows * group;
-  const bool tc = nq > kTcQueries;
+  const bool tc = nq > 32 && (long long)n_kv * ((nq + 31) / 32) * slots >= kTcWork;
   const int qb = tc ? (io == 2 ? 128 : 256) : 8 * query_eights(nq);
   const int blocks = n_kv * ((nq + qb - 1) / qb);
   const int slots_a_tile = tc ? 128 : kTileSlots;
@@ -842,11 +845,11 @@ Kv8Splits kv8_attention_splits(int rows, int group, int n_kv, int slots, int io)
   if (n <= 1) return {1, false, tc};
   const int per = (tiles + n - 1) / n;
   n = (tiles + per - 1) / per;                             // no split without a tile
-  // A GPC of sixteen SMs holds fifteen or sixteen CTAs in clusters of up to five, but twelve in clusters of six; where
-  // the CTAs would fill half the chip, larger clusters run in two waves (72 queries a head over 4000 slots: 34.2 us in
-  // clusters of six, 21.5 us for 128 queries in clusters of four).
-  const bool cluster = n <= 5 || (n <= kMaxCluster && n * blocks <= 76);
-  return {n, tc || !cluster, tc};
+  // A GPC's sixteen to twenty SMs hold few whole clusters: past these counts the launch runs in two waves (72 queries a
+  // head over 4000 slots: 34.2 us as 144 CTAs in clusters of six, 18.7 merged through scratch; 192 queries: 49.3 us as 144
+  // CTAs in clusters of three).
+  const bool cluster = !tc && n <= kMaxCluster && n * blocks <= (n <= 4 ? 128 : 76);
+  return {n, !cluster, tc};
 }
 
 bool launch_kv8_attention(const Kv8AttnArgs& a, int io, bool tc, cudaStream_t st) {

@@ -48,7 +48,7 @@ def score_error(q, k, scale, cap):
     kk = np.repeat(np.abs(k.astype(np.float64)), group, 1)
     aq = np.abs(q.astype(np.float64))
     rest = 2.0 ** -21 * aq.max(-1)[..., None] * kk.sum(-1).T[None]
-    mags = np.einsum("rhd,nhd->rhn", aq, kk)
+    mags = np.matmul(aq.transpose(1, 0, 2), kk.transpose(1, 2, 0)).transpose(1, 0, 2)
     return scale * (rest + 24 * 2.0 ** -23 * mags + 4 * U24 * mags) + (8 * 2.0 ** -23 * cap if cap else 0.0)
 
 
@@ -64,7 +64,8 @@ def out_error(q, k, v, vis, want, scale, cap, io):
     m = s.max(-1, keepdims=True)
     p = np.exp(s - np.where(np.isfinite(m), m, 0.0))
     total = np.maximum(p.sum(-1), 1e-300)
-    mean_v = np.einsum("rhn,nhd->rhd", p, np.where(vis.any(0)[:, None, None], vv, 0.0)) / total[..., None]
+    seen = np.where(vis.any(0)[:, None, None], vv, 0.0)
+    mean_v = np.matmul(p.transpose(1, 0, 2), seen.transpose(1, 0, 2)).transpose(1, 0, 2) / total[..., None]
     top = np.where(vis.any(0)[:, None, None], vv, 0.0).max((0, 2))[None, :]
     rel = 2 * (2 * e + 2.0 ** -22 * (1 + np.abs(np.where(np.isfinite(m[..., 0]), m[..., 0], 0.0)))) + (n / 16 + 200) * 2.0 ** -23
     rel = rel + (2.0 ** -21 if io == "fp32" else 2.0 ** -11)

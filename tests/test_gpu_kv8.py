@@ -162,15 +162,18 @@ ATTN = [  # rows, prefix, base - prefix, masks, hq, hkv, hd, code, block, io, ca
     (5, 200, 213, "own", 16, 2, 128, "e4m3", 64, "fp32", 0.0),  # the DP rows' slots, past the committed ones
     (64, 128, 0, "causal", 8, 8, 64, "int8", 32, "fp32", 0.0),
     (64, 1000, 0, "holes", 64, 8, 128, "int8", 64, "bf16", 0.0),
-    # more than 64 queries for a KV head: the tensor-core kernel, with one or two query blocks, whole and ragged
-    (64, 300, 0, "causal", 16, 8, 128, "e4m3", 32, "bf16", 0.0),
     (33, 1, 0, "tree", 8, 2, 128, "int8", 16, "fp16", 0.0),
     (17, 5000, 0, "tree", 40, 5, 128, "int8", 64, "fp32", 0.0),
-    (64, 130, 70, "holes", 24, 4, 64, "e4m3", 16, "fp32", 30.0),
-    (64, 2049, 0, "causal", 32, 4, 64, "int8", 32, "bf16", 50.0),
-    (40, 0, 0, "causal", 16, 4, 128, "e4m3", 64, "fp32", 0.0),
-    (64, 0, 0, "none", 8, 4, 64, "int8", 64, "fp16", 0.0),
-    (31, 9000, -20, "tree", 27, 3, 128, "int8", 32, "fp32", 0.0),
+    (31, 4000, -20, "tree", 27, 3, 128, "int8", 32, "fp32", 0.0),
+    # many queries over many slots: the tcgen05 kernel, with one or two query blocks, whole and ragged
+    (64, 1600, 0, "causal", 64, 64, 64, "e4m3", 32, "bf16", 0.0),
+    (64, 3100, 70, "holes", 48, 8, 64, "e4m3", 16, "fp32", 30.0),
+    (33, 6300, 0, "tree", 32, 8, 128, "int8", 16, "fp16", 0.0),
+    (16, 6272, 0, "causal", 64, 8, 128, "int8", 64, "bf16", 50.0),
+    (9, 25000, 0, "tree", 16, 4, 128, "int8", 32, "fp32", 0.0),
+    (64, 4300, -20, "tree", 24, 3, 128, "e4m3", 64, "fp16", 0.0),
+    (40, 100013, 0, "own", 1, 1, 64, "int8", 32, "bf16", 0.0),
+    (64, 0, 3300, "holes", 40, 40, 64, "int8", 64, "fp32", 0.0),
     (3, 0, 0, "holes", 6, 3, 64, "e4m3", 16, "fp32", 0.0),  # a row that sees nothing
     (9, 77, 40, "none", 10, 10, 128, "int8", 16, "fp16", 0.0),
     (6, 100, -10, "tree", 21, 3, 64, "int8", 32, "fp32", 50.0),  # new slots that the prefix holds already count once
