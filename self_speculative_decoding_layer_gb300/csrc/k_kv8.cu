@@ -109,6 +109,8 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_kv8_append(Kv8View c, Kv8R
   __shared__ uint32_t red[3][32];
   const int h = blockIdx.y;
   const int rshift = c.hd == 128 ? 3 : 2;  // 2^rshift chunks a row
+  griddep_launch();
+  griddep_wait();
   const int slot0 = ((a.first >> c.tshift) + blockIdx.x) << c.tshift;
   const int page = c.btab[slot0 / kPage];
   const int t = threadIdx.x >> rshift, row = slot0 + t - a.first;
@@ -148,6 +150,8 @@ __global__ void __launch_bounds__(256) k_kv8_read(Kv8View c, Kv8RowsArgs a, int 
   const int per_row = c.hd / N, per_slot = per_row * c.n_kv;
   const int which = blockIdx.y;
   const int slot0 = (a.first / run + blockIdx.x) * run;
+  griddep_launch();
+  griddep_wait();
   const int page = c.btab[slot0 / kPage];
   const bool ok = c.page_ok(page);
   const int r0 = max(0, a.first - slot0), r1 = min(run, a.first + a.rows - slot0);
@@ -232,6 +236,7 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
   const int rank = cl.block_rank(), nr = cl.num_blocks();
   const int h = blockIdx.y, tid = threadIdx.x;
   griddep_launch();
+  griddep_wait();
   const float* w = a.weight + (size_t)h * a.ld_weight;
   const int cand = a.n - a.recent, want = a.keep - a.recent;
   int* index = a.index + (size_t)h * a.keep;
@@ -362,6 +367,7 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_kv8_gather(Kv8View src, Kv
   const int h = blockIdx.y;
   const int rshift = dst.hd == 128 ? 3 : 2;
   const int slot0 = blockIdx.x << dst.tshift;
+  griddep_launch();
   griddep_wait();
   const int page = dst.btab[slot0 / kPage];
   const int t = threadIdx.x >> rshift;
@@ -406,13 +412,8 @@ bool launch_kv8_append(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStrea
   const int t0 = a.first >> c.tshift, t1 = (a.first + a.rows - 1) >> c.tshift;
   const dim3 grid(t1 - t0 + 1, c.n_kv);
   const int threads = (c.hd / 16) << c.tshift;
-  if (io == 0)
-    k_kv8_append<__nv_bfloat16><<<grid, threads, 0, st>>>(c, a);
-  else if (io == 1)
-    k_kv8_append<__half><<<grid, threads, 0, st>>>(c, a);
-  else
-    k_kv8_append<float><<<grid, threads, 0, st>>>(c, a);
-  return cudaGetLastError() == cudaSuccess;
+  return launch_kv8(io == 0 ? k_kv8_append<__nv_bfloat16> : io == 1 ? k_kv8_append<__half> : k_kv8_append<float>, grid,
+                    threads, 0, st, 1, c, a);
 }
 
 bool launch_kv8_read(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st) {
@@ -422,13 +423,8 @@ bool launch_kv8_read(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_
   int run = 16;  // shorter runs where sixteen would leave an SM without eight CTAs
   while (run > 1 && (long long)a.rows / run * 2 * parts < 8 * 152) run /= 2;
   const dim3 grid((a.first + a.rows - 1) / run - a.first / run + 1, 2, parts);
-  if (io == 0)
-    k_kv8_read<__nv_bfloat16><<<grid, threads, 0, st>>>(c, a, run);
-  else if (io == 1)
-    k_kv8_read<__half><<<grid, threads, 0, st>>>(c, a, run);
-  else
-    k_kv8_read<float><<<grid, threads, 0, st>>>(c, a, run);
-  return cudaGetLastError() == cudaSuccess;
+  return launch_kv8(io == 0 ? k_kv8_read<__nv_bfloat16> : io == 1 ? k_kv8_read<__half> : k_kv8_read<float>, grid, threads,
+                    0, st, 1, c, a, run);
 }
 
 bool launch_kv8_evict(const Kv8View& src, const Kv8View& dst, const Kv8SelectArgs& a, cudaStream_t st) {
@@ -436,24 +432,11 @@ bool launch_kv8_evict(const Kv8View& src, const Kv8View& dst, const Kv8SelectArg
   int nr = 1;  // CTAs of a head: enough that a thread has few keys, eight at most
   while (nr < kSelCluster && cand > nr * kSelThreads * 4) nr *= 2;
   const bool reload = cand > nr * kSelThreads * kSelKeys;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = nr;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(nr, src.n_kv);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, reload ? k_kv8_select<true> : k_kv8_select<false>, a) != cudaSuccess) return false;
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(((a.keep - 1) >> dst.tshift) + 1, src.n_kv);
-  cfg.blockDim = dim3((dst.hd / 16) << dst.tshift);
-  return cudaLaunchKernelEx(&cfg, src.code == KV8_INT8 ? k_kv8_gather<KV8_INT8> : k_kv8_gather<KV8_E4M3>, src, dst,
-                            (const int*)a.index, a.keep) == cudaSuccess;
+  if (!launch_kv8(reload ? k_kv8_select<true> : k_kv8_select<false>, dim3(nr, src.n_kv), kSelThreads, 0, st, nr, a))
+    return false;
+  return launch_kv8(src.code == KV8_INT8 ? k_kv8_gather<KV8_INT8> : k_kv8_gather<KV8_E4M3>,
+                    dim3(((a.keep - 1) >> dst.tshift) + 1, src.n_kv), (dst.hd / 16) << dst.tshift, 0, st, 1, src, dst,
+                    (const int*)a.index, a.keep);
 }
 
 }  // namespace ssd

@@ -188,6 +188,7 @@ __global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(
   const int split = blockIdx.x, h = blockIdx.y, q0 = blockIdx.z * QB;
   const int nq = a.rows * a.group;
   griddep_launch();
+  griddep_wait();
 
   const Tiles<5> tiles(a.prefix, a.base, a.rows);
   const int t_first = split * a.split_tiles, t_last = min(tiles.n, t_first + a.split_tiles);
@@ -541,6 +542,7 @@ __global__ void __launch_bounds__(HD) k_kv8_merge(const __grid_constant__ Kv8Att
   const int nq = a.rows * a.group;
   const int i = blockIdx.x;
   const int h = i / nq, qi = i - h * nq, r = qi / a.group, head = h * a.group + qi - r * a.group;
+  griddep_launch();
   griddep_wait();
   const float2* ml = a.part_ml + (size_t)i * a.n_split;
   const float* po = a.part_o + (size_t)i * a.n_split * HD + threadIdx.x;
@@ -607,6 +609,8 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
   const int n_tiles = (n_slots + 15) >> 4, stride = gridDim.x * kWWarps;
   const int first = blockIdx.x * kWWarps + warp;
   const int nq = a.n_take * a.group;
+  griddep_launch();
+  griddep_wait();
 
   // Page of tile ti, or -1 where it has none or no row sees it.
   auto page_of = [&](int ti) {
@@ -747,22 +751,8 @@ bool run_attention(Kv8AttnArgs a, cudaStream_t st) {
   const auto kern = k_kv8_attention<T, HD, CODE, QT>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) != cudaSuccess) return false;
   const int nq = a.rows * a.group;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3(a.n_split, a.c.n_kv, (nq + L::QB - 1) / L::QB);
-  cfg.blockDim = dim3(L::W * 32);
-  cfg.dynamicSmemBytes = L::kBytes;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 0;
-  if (!a.part_o && a.n_split > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.n_split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
-  }
-  return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess;
+  return launch_kv8(kern, dim3(a.n_split, a.c.n_kv, (nq + L::QB - 1) / L::QB), L::W * 32, L::kBytes, st,
+                    a.part_o ? 1 : a.n_split, a);
 }
 
 // Query eights of a CTA: all of a KV head's queries up to four eights.
@@ -786,26 +776,15 @@ bool run_weights(const Kv8AttnArgs& a, cudaStream_t st) {
   int fit = 2 * 152 / a.c.n_kv;                                       // two CTAs on each of 152 SMs
   if (fit < 1) fit = 1;
   const dim3 grid(groups < fit ? groups : fit, a.c.n_kv);
-  if (a.cap > 0.f)
-    k_kv8_weights<T, HD, CODE, true><<<grid, kWWarps * 32, smem, st>>>(a, n_slots);
-  else
-    k_kv8_weights<T, HD, CODE, false><<<grid, kWWarps * 32, smem, st>>>(a, n_slots);
-  return cudaGetLastError() == cudaSuccess;
+  return launch_kv8(a.cap > 0.f ? k_kv8_weights<T, HD, CODE, true> : k_kv8_weights<T, HD, CODE, false>, grid, kWWarps * 32,
+                    smem, st, 1, a, n_slots);
 }
 
 // Add up the splits of scratch.
 template <typename T>
 bool run_merge(const Kv8AttnArgs& a, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(a.c.n_kv * a.rows * a.group);
-  cfg.blockDim = dim3(a.c.hd);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, a.c.hd == 128 ? k_kv8_merge<T, 128> : k_kv8_merge<T, 64>, a) == cudaSuccess;
+  return launch_kv8(a.c.hd == 128 ? k_kv8_merge<T, 128> : k_kv8_merge<T, 64>, a.c.n_kv * a.rows * a.group, a.c.hd, 0, st, 1,
+                    a);
 }
 
 template <typename T>

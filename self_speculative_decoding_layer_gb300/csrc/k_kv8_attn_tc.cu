@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
       fence_barrier_init();
     }
   }
+  griddep_wait();
   // Converters: thread ct takes sixteen-byte chunk ct % CH of rows ct / CH + RS i of every tile.  What they need
   // first is asked for before the queries are staged.
   constexpr int CH = HD / 16, RS = kConvWarps * 32 / CH, NI = 128 / RS;
@@ -571,8 +572,7 @@ bool run_tc(Kv8AttnArgs a, cudaStream_t st) {
   const Tiles<7> tiles(a.prefix, a.base, a.rows);
   a.split_tiles = (tiles.n + a.n_split - 1) / a.n_split;
   const int qb = 128 * L::NQT, nq = a.rows * a.group;
-  kern<<<dim3(a.n_split, a.c.n_kv, (nq + qb - 1) / qb), kTcThreads, L::kBytes, st>>>(a);
-  return cudaGetLastError() == cudaSuccess;
+  return launch_kv8(kern, dim3(a.n_split, a.c.n_kv, (nq + qb - 1) / qb), kTcThreads, L::kBytes, st, 1, a);
 }
 
 template <typename T>

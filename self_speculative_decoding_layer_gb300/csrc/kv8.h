@@ -8,6 +8,29 @@
 
 namespace ssd {
 
+// Launch with programmatic serialization: the kernel may start while its predecessor in the stream drains, and each of
+// these kernels calls griddep_wait() in every thread before it touches global memory.  cluster > 1: clusters of that
+// many CTAs along x.  False if the launch failed.
+template <typename... KArgs, typename... Args>
+inline bool launch_kv8(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, int cluster,
+                       const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess;
+}
+
 // Rows to append to a cache (k, v are read) or values to read from it (k, v are written), 16-byte aligned.
 struct Kv8RowsArgs {
   void* k;
