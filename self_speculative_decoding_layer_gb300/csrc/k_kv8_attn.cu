@@ -136,6 +136,8 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+constexpr bool cluster_fits(int queries, bool fp32) { return queries < 32 || !fp32; }
+
 // Warps of a CTA and stages of a warp's ring.  Eight queries leave registers for twelve warps, which hide the
 // latency of the conversions, with two stages each (8 KB under way a warp, 96 KB an SM); the larger blocks run
 // eight warps with three.
@@ -156,7 +158,10 @@ struct AttnSmem {
   static constexpr int OS = HD + 4;                                         // row stride of the merge buffers
   static constexpr int kMerge = W * QB * OS * 4;                            // over the ring, after the loop
   static constexpr int kHead = W * R::kStages * 32;                         // tile headers (TileHead)
-  static constexpr int kBytes = kQ + (kRing > kMerge ? kRing : kMerge) + kHead;
+  // partial results that the other CTAs of a cluster send (32 fp32 queries leave no room, and use scratch)
+  static constexpr int kPart = cluster_fits(QB, sizeof(T) == 4) ? (QB * HD / 4 + kMaxCluster) * 16 : 0;
+  static constexpr int kLoop = kQ + (kRing > kMerge ? kRing : kMerge);
+  static constexpr int kBytes = kLoop + kHead + kPart;
 };
 
 struct __align__(16) TileHead {
@@ -187,13 +192,15 @@ __global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int split = blockIdx.x, h = blockIdx.y, q0 = blockIdx.z * QB;
   const int nq = a.rows * a.group;
+  const bool clustered = !a.part_o && a.n_split > 1;
+  if (clustered) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // waited for before the merge
   griddep_launch();
   griddep_wait();
 
   const Tiles<5> tiles(a.prefix, a.base, a.rows);
   const int t_first = split * a.split_tiles, t_last = min(tiles.n, t_first + a.split_tiles);
   const unsigned char* ring = s_dyn + L::kQ + warp * R::kWarp;
-  TileHead* heads = reinterpret_cast<TileHead*>(s_dyn + L::kBytes - L::kHead) + warp * R::kStages;
+  TileHead* heads = reinterpret_cast<TileHead*>(s_dyn + L::kLoop) + warp * R::kStages;
 
   // Tile ti (physical page `page`) into ring stage st; one group of copies whether or not there is a tile.
   auto fill = [&](int st, int ti, int page) {
@@ -498,39 +505,40 @@ __global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(
       const int q = i / (HD / 4), d = (i % (HD / 4)) * 4;
       output(q, d, mine[j], s_ml[q].x, s_ml[q].y);
     }
-  } else {  // the cluster's partial results lie in its CTAs' shared memory; rank r adds every n_split-th item
+  } else if constexpr (L::kPart > 0) {
+    // The cluster's partial results: rank r adds every n_split-th item, which the others put into its shared memory
+    // (a buffer of its own, since r may still be working on its tiles).
     cg::cluster_group cl = cg::this_cluster();
+    float4* s_part = reinterpret_cast<float4*>(s_dyn + L::kLoop + L::kHead);  // [ranks][items of this rank]
+    const int n = a.n_split, per = (ITEMS + n - 1) / n;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA of the cluster has started
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int i = threadIdx.x + j * W * 32;
-      if (i < ITEMS) *reinterpret_cast<float4*>(s_o + i * 4) = mine[j];
+      if (i < ITEMS) cl.map_shared_rank(s_part, i % n)[split * per + i / n] = mine[j];
     }
+    for (int i = threadIdx.x; i < QB * n; i += W * 32) cl.map_shared_rank(&s_f[split][i % QB], i / QB)[0] = s_ml[i % QB];
     cl.sync();
-    for (int i = threadIdx.x; i < QB * a.n_split; i += W * 32) s_f[i / QB][i % QB] = cl.map_shared_rank(s_ml, i / QB)[i % QB];
-    __syncthreads();
-    for (int i = split + threadIdx.x * a.n_split; i < ITEMS; i += W * 32 * a.n_split) {
-      const int q = i / (HD / 4), d = (i % (HD / 4)) * 4;
-      float4 y[kMaxCluster];
+    for (int k = threadIdx.x; k * n + split < ITEMS; k += W * 32) {
+      const int i = k * n + split, q = i / (HD / 4), d = (i % (HD / 4)) * 4;
       float M = -INFINITY;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r)
-        if (r < a.n_split) {
-          y[r] = *reinterpret_cast<const float4*>(cl.map_shared_rank(s_o, r) + i * 4);
-          M = fmaxf(M, s_f[r][q].x);
-        }
+        if (r < n) M = fmaxf(M, s_f[r][q].x);
       const float ref = M == -INFINITY ? 0.f : M;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f;
 #pragma unroll
       for (int r = 0; r < kMaxCluster; ++r)
-        if (r < a.n_split) {
-          const float f = exp2_approx(s_f[r][q].x - ref);
-          x.x += y[r].x * f, x.y += y[r].y * f, x.z += y[r].z * f, x.w += y[r].w * f;
-          sum += s_f[r][q].y * f;
+        if (r < n) {
+          const float2 ml = s_f[r][q];
+          const float f = exp2_approx(ml.x - ref);
+          const float4 y = s_part[r * per + k];
+          x.x += y.x * f, x.y += y.y * f, x.z += y.z * f, x.w += y.w * f;
+          sum += ml.y * f;
         }
       output(q, d, x, M, sum);
     }
-    cl.sync();  // no CTA leaves while another may read its shared memory
   }
 }
 
@@ -827,7 +835,7 @@ Kv8Splits kv8_attention_splits(int rows, int group, int n_kv, int slots, int io)
   // A GPC's sixteen to twenty SMs hold few whole clusters: past these counts the launch runs in two waves (72 queries a
   // head over 4000 slots: 34.2 us as 144 CTAs in clusters of six, 18.7 merged through scratch; 192 queries: 49.3 us as 144
   // CTAs in clusters of three).
-  const bool cluster = !tc && n <= kMaxCluster && n * blocks <= (n <= 4 ? 128 : 76);
+  const bool cluster = !tc && cluster_fits(qb, io == 2) && n <= kMaxCluster && n * blocks <= (n <= 4 ? 128 : 76);
   return {n, !cluster, tc};
 }
 
