@@ -620,19 +620,15 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
   griddep_launch();
   griddep_wait();
 
-  // Page of tile ti, or -1 where it has none or no row sees it.
-  auto page_of = [&](int ti) {
-    if (ti >= n_tiles || !visible_any(ti * 16, a)) return -1;
-    const int page = __ldg(a.c.btab + ti * 16 / kPage);
-    return a.c.page_ok(page) ? page : -1;
-  };
+  // Page of tile ti as the table has it (checked where it is used, a tile later), or -1 where no row sees the tile.
+  auto page_of = [&](int ti) { return ti < n_tiles && visible_any(ti * 16, a) ? __ldg(a.c.btab + ti * 16 / kPage) : -1; };
   struct Tile {
     uint4 lo[NJ], hi[NJ];  // codes of rows g and g + 8
     float ks;
     bool live;
   };
   auto load = [&](Tile& t, int ti, int page) {
-    t.live = page >= 0;
+    t.live = a.c.page_ok(page);
     if (!t.live) return;
     const int in_page = ti * 16 % kPage;
     const size_t row0 = a.c.page_row(page, h) + (size_t)(in_page + g) * HD + c * 16;
@@ -646,10 +642,9 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
 
   for (int q0 = 0; q0 == 0 || q0 < nq; q0 += kWEights * 8) {
     const int eights = nq ? min(kWEights, (nq - q0 + 7) / 8) : 0;
-    Tile cur, next;  // two tiles' codes are on their way while one is worked on
+    Tile cur;
     load(cur, first, page_of(first));
-    load(next, first + stride, page_of(first + stride));
-    int page = page_of(first + 2 * stride);
+    int page = page_of(first + stride);
     if (q0) __syncthreads();
 #pragma unroll 4
     for (int q = warp; q < eights * 8; q += kWWarps) {
@@ -686,9 +681,8 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
           codes_to_half<CODE>(word_of(cur.hi[i >> 2], i & 3), k[i][1], k[i][3]);
         }
       }
-      cur = next;
-      load(next, ti + 2 * stride, page);
-      page = page_of(ti + 3 * stride);
+      load(cur, ti + stride, page);
+      page = page_of(ti + 2 * stride);
       const int slot = slot0 + g + c * 8;  // of lanes c = 0 and 1
       const size_t at = (size_t)h * a.ld_w + slot;
       const bool mine = c < 2 && slot < n_slots;
@@ -724,7 +718,7 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
         }
       };
       if (live && slot0 + 16 <= a.prefix) {
-#pragma unroll 2
+#pragma unroll 4
         for (int t = 0; t < eights; ++t) {
           float x[4];
           weigh(t, x);

@@ -191,15 +191,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
   // first is asked for before the queries are staged.
   constexpr int CH = HD / 16, RS = kConvWarps * 32 / CH, NI = 128 / RS;
   const int ct = threadIdx.x - 256, ch = ct & (CH - 1), r0 = (ct & (kConvWarps * 32 - 1)) / CH;
-  // Page `half` of tile j; -1 where it is none or no row sees a slot of it.
+  // Page `half` of tile j as the table has it (checked where it is used, a tile later), or -1 where no row sees a slot
+  // of it.
   auto page_of = [&](int j, int half) {
     if (j >= n_tile) return -1;
     const int slot = tiles.slot(t_first + j) + half * kPage;
     if (!visible_any(slot, a) && !visible_any(slot + 16, a) && !visible_any(slot + 32, a) && !visible_any(slot + 48, a))
       return -1;
-    const int page = __ldg(a.c.btab + slot / kPage);
-    return a.c.page_ok(page) ? page : -1;
+    return __ldg(a.c.btab + slot / kPage);
   };
+  auto checked = [&](int page) { return a.c.page_ok(page) ? page : -1; };
   uint4 k[NI], v[NI];
   // Byte offset of this thread's first chunk in a page's rows of this head.
   auto page_at = [&](int page) { return page < 0 ? (size_t)0 : a.c.page_row(page, h) + (size_t)r0 * HD + ch * 16; };
@@ -217,8 +218,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
   const bool converter = warp >= 8 && warp < kMmaWarp;
   int p0 = -1, p1 = -1;
   if (converter && n_tile > 0) {
-    p0 = page_of(0, 0);
-    p1 = page_of(0, 1);
+    p0 = checked(page_of(0, 0));
+    p1 = checked(page_of(0, 1));
     const size_t a0 = page_at(p0), a1 = page_at(p1);
 #pragma unroll
     for (int i = 0; i < NI; ++i) load(i, 0, RS * i < kPage ? p0 : p1, RS * i < kPage ? a0 : a1, whole_of(0));
@@ -279,9 +280,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
     const float vref = vmax > 0.f ? vmax : 1.f;
     if (ct == 0) s_vref = vref;
 
-    int n0 = page_of(1, 0), n1 = page_of(1, 1);
+    int t0 = page_of(1, 0), t1 = page_of(1, 1);
     for (int j = 0; j < n_tile; ++j) {
-      const int st = j & 1;
+      const int st = j & 1, n0 = checked(t0), n1 = checked(t1);
+      t0 = page_of(j + 2, 0);
+      t1 = page_of(j + 2, 1);
       float ks = 0.f, vs = 0.f;  // of sixteen slots, for eight of the threads
       const int slot0 = tiles.slot(t_first + j);
       if (ct < 8) {
@@ -299,15 +302,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
       // Chunk i becomes two sixteen-byte chunks of fp16 for K and for V, stored in an order that alternates with the
       // 64-wide block, so that a row's lanes meet in no bank.  (r0 + RS i and r0 have the same three low bits.)
       const int flip = ch >> 2, c0 = (ch & 3) * 2;
-      const uint32_t t0 = (uint32_t)((c0 + flip) ^ (r0 & 7)) << 4, t1 = (uint32_t)((c0 + 1 - flip) ^ (r0 & 7)) << 4;
+      const uint32_t o0 = (uint32_t)((c0 + flip) ^ (r0 & 7)) << 4, o1 = (uint32_t)((c0 + 1 - flip) ^ (r0 & 7)) << 4;
       auto convert = [&](const uint4& u, unsigned char* to) {
         uint4 w0, w1;
         codes_to_half<CODE>(flip ? u.z : u.x, w0.x, w0.y);
         codes_to_half<CODE>(flip ? u.w : u.y, w0.z, w0.w);
         codes_to_half<CODE>(flip ? u.x : u.z, w1.x, w1.y);
         codes_to_half<CODE>(flip ? u.y : u.w, w1.z, w1.w);
-        *reinterpret_cast<uint4*>(to + t0) = w0;
-        *reinterpret_cast<uint4*>(to + t1) = w1;
+        *reinterpret_cast<uint4*>(to + o0) = w0;
+        *reinterpret_cast<uint4*>(to + o1) = w1;
       };
       if (whole && n0 >= 0 && n1 >= 0) {
         const uint8_t *k0 = a.c.k + a0, *k1 = a.c.k + a1, *v0 = a.c.v + a0, *v1 = a.c.v + a1;
@@ -340,8 +343,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
       arrive(&kv_full[st]);
       p0 = n0;
       p1 = n1;
-      n0 = page_of(j + 2, 0);
-      n1 = page_of(j + 2, 1);
     }
   } else if (warp == kMmaWarp) {
     if (n_tile > 0) {
