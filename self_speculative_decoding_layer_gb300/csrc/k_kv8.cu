@@ -34,17 +34,34 @@ __device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
   }
 }
 
-__device__ __forceinline__ void decode16(const uint4& u, float s, int code, float (&x)[16]) {
-  decode4(u.x, s, code, x);
-  decode4(u.y, s, code, x + 4);
-  decode4(u.z, s, code, x + 8);
-  decode4(u.w, s, code, x + 12);
+template <int CODE>
+__device__ __forceinline__ void decode16(const uint4& u, float s, float (&x)[16]) {
+  decode4<CODE>(u.x, s, x);
+  decode4<CODE>(u.y, s, x + 4);
+  decode4<CODE>(u.z, s, x + 8);
+  decode4<CODE>(u.w, s, x + 12);
 }
 
-template <bool ODD>
-__device__ __forceinline__ uint4 encode16(const float (&x)[16], float m, int code) {
-  return make_uint4(encode4<ODD>(x, m, code), encode4<ODD>(x + 4, m, code), encode4<ODD>(x + 8, m, code),
-                    encode4<ODD>(x + 12, m, code));
+template <int CODE, bool ODD>
+__device__ __forceinline__ uint4 encode16(const float (&x)[16], float m) {
+  return make_uint4(encode4<CODE, ODD>(x, m), encode4<CODE, ODD>(x + 4, m), encode4<CODE, ODD>(x + 8, m),
+                    encode4<CODE, ODD>(x + 12, m));
+}
+// Values that may hold a NaN or an infinity: out of line, so that the usual path is not computed beside it.
+template <int CODE>
+__device__ __noinline__ uint4 encode16_odd(float x0, float x1, float x2, float x3, float x4, float x5, float x6, float x7,
+                                           float x8, float x9, float x10, float x11, float x12, float x13, float x14, float x15,
+                                           float m) {
+  const float x[16] = {x0, x1, x2, x3, x4, x5, x6, x7, x8, x9, x10, x11, x12, x13, x14, x15};
+  return encode16<CODE, true>(x, m);
+}
+template <int CODE>
+__device__ __forceinline__ void store_codes(uint8_t* to, const float (&x)[16], float m, bool odd) {
+  if (odd)
+    *reinterpret_cast<uint4*>(to) = encode16_odd<CODE>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], x[8], x[9], x[10],
+                                                       x[11], x[12], x[13], x[14], x[15], m);
+  else
+    *reinterpret_cast<uint4*>(to) = encode16<CODE, false>(x, m);
 }
 
 // The larger of a and the magnitudes of x (NaN compares as absent), and a number that is NaN if x holds a NaN or an
@@ -80,31 +97,9 @@ __device__ __forceinline__ bool block_max2(float& a, float& b, float odd, uint32
   return __any_sync(0xffffffffu, lane < warps && red[2][lane]);
 }
 
-// Quantise a block of K (x[0], magnitudes up to amax[0]) and of V (x[1]): a chunk of sixteen values for each thread
-// with `used`, whose scales come from those with `counts` and are no smaller than least; write scales and codes.
-__device__ __forceinline__ void quantise(const float (&x)[2][16], float (&amax)[2], float odd, bool counts, bool used,
-                                         const float (&least)[2], int code, uint8_t* const (&to)[2], float* const (&scale)[2],
-                                         uint32_t (&red)[3][32]) {
-  // (the barrier also orders every read of kept codes and scales before the writes)
-  const bool any_odd = block_max2(amax[0], amax[1], odd, red);
-  if (any_odd) {
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 2; ++w) amax[w] = counts ? finite_amax16(x[w], 0.f) : 0.f;
-    block_max2(amax[0], amax[1], 0.f, red);
-  }
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const float s = fmaxf(block_scale(amax[w], code), least[w]);
-    const float m = inverse_scale(s);
-    if (used) *reinterpret_cast<uint4*>(to[w]) = any_odd ? encode16<true>(x[w], m, code) : encode16<false>(x[w], m, code);
-    if (threadIdx.x == 0) *scale[w] = s;
-  }
-}
-
 // Grid (blocks of T tokens, KV heads).  A block holds T * hd / 16 chunks of sixteen values (64..512) of K and of V, one
 // of each for every thread.
-template <typename T>
+template <typename T, int CODE>
 __global__ void __launch_bounds__(kQuantThreads, 2) k_kv8_append(Kv8View c, Kv8RowsArgs a) {
   __shared__ uint32_t red[3][32];
   const int h = blockIdx.y;
@@ -133,18 +128,31 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_kv8_append(Kv8View c, Kv8R
     least[1] = c.vs[sc];
     if (row < 0) {
       float unused = 0.f;
-      decode16(*reinterpret_cast<const uint4*>(c.k + at), least[0], c.code, x[0]);
-      decode16(*reinterpret_cast<const uint4*>(c.v + at), least[1], c.code, x[1]);
+      decode16<CODE>(*reinterpret_cast<const uint4*>(c.k + at), least[0], x[0]);
+      decode16<CODE>(*reinterpret_cast<const uint4*>(c.v + at), least[1], x[1]);
       amax16(x[0], unused, odd);
       amax16(x[1], unused, odd);
     }
   }
-  quantise(x, amax, odd, fresh, row < a.rows, least, c.code, {c.k + at, c.v + at}, {c.ks + sc, c.vs + sc}, red);
+  // (the barrier also orders every read of kept codes and scales before the writes)
+  const bool any_odd = block_max2(amax[0], amax[1], odd, red);
+  if (any_odd) {
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 2; ++w) amax[w] = fresh ? finite_amax16(x[w], 0.f) : 0.f;
+    block_max2(amax[0], amax[1], 0.f, red);
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const float s = fmaxf(block_scale<CODE>(amax[w]), least[w]);
+    if (row < a.rows) store_codes<CODE>((w ? c.v : c.k) + at, x[w], inverse_scale(s), any_odd);
+    if (threadIdx.x == 0) (w ? c.vs : c.ks)[sc] = s;
+  }
 }
 
 // Grid (runs of `run` slots, a divisor of sixteen, so that they share a scale; K / V; parts of a row).  A thread makes sixteen bytes of output (4 fp32 or 8 16-bit
 // values) at a time.
-template <typename T>
+template <typename T, int CODE>
 __global__ void __launch_bounds__(256) k_kv8_read(Kv8View c, Kv8RowsArgs a, int run) {
   constexpr int N = 16 / sizeof(T);
   const int per_row = c.hd / N, per_slot = per_row * c.n_kv;
@@ -169,7 +177,7 @@ __global__ void __launch_bounds__(256) k_kv8_read(Kv8View c, Kv8RowsArgs a, int 
       float x[N];
 #pragma unroll
       for (int e = 0; e < N; e += 4)
-        decode4(ok ? __ldg(reinterpret_cast<const uint32_t*>(p + r * c.hd + e)) : 0u, s, c.code, x + e);
+        decode4<CODE>(ok ? __ldg(reinterpret_cast<const uint32_t*>(p + r * c.hd + e)) : 0u, s, x + e);
       T* o = to + (size_t)r * ld + (size_t)i * N;
       if constexpr (sizeof(T) == 4) {
         *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
@@ -360,9 +368,10 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
   cl.sync();  // no CTA leaves while another may read its counters
 }
 
-// Grid (blocks of the kept slots, heads).
-template <int CODE>
-__global__ void __launch_bounds__(kQuantThreads, 2) k_kv8_gather(Kv8View src, Kv8View dst, const int* index, int keep) {
+// Grid (blocks of the kept slots, heads).  A thread keeps its two chunks as codes, not values, over the reduction: a
+// row's index, page and codes are three round trips to memory, and what bounds the kernel is how many are under way.
+template <int FROM, int TO>
+__global__ void __launch_bounds__(kQuantThreads, 3) k_kv8_gather(Kv8View src, Kv8View dst, const int* index, int keep) {
   __shared__ uint32_t red[3][32];
   const int h = blockIdx.y;
   const int rshift = dst.hd == 128 ? 3 : 2;
@@ -372,38 +381,50 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_kv8_gather(Kv8View src, Kv
   const int page = dst.btab[slot0 / kPage];
   const int t = threadIdx.x >> rshift;
   const bool used = slot0 + t < keep;
-  float x[2][16];
-  float amax[2] = {0.f, 0.f}, odd = 0.f;
+  uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+  float from[2] = {0.f, 0.f}, amax[2] = {0.f, 0.f}, odd = 0.f;
   if (used) {
     const int slot = __ldg(index + (size_t)h * keep + slot0 + t);
     const int p = __ldg(src.btab + slot / kPage), in_page = slot % kPage;
-    uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-    float s[2] = {0.f, 0.f};
     if (src.page_ok(p)) {
       const size_t at = src.page_row(p, h) + (size_t)in_page * src.hd + (threadIdx.x - (t << rshift)) * 16;
       const size_t sc = src.scale_at(p, h, in_page);
       u[0] = __ldg(reinterpret_cast<const uint4*>(src.k + at));
       u[1] = __ldg(reinterpret_cast<const uint4*>(src.v + at));
-      s[0] = __ldg(src.ks + sc);
-      s[1] = __ldg(src.vs + sc);
+      from[0] = __ldg(src.ks + sc);
+      from[1] = __ldg(src.vs + sc);
     }
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      decode16(u[w], s[w], CODE, x[w]);
-      if (CODE == KV8_INT8) {  // int8 codes are numbers: a value is odd only where its scale is, or its product
-#pragma unroll
-        for (int i = 0; i < 16; ++i) amax[w] = fmaxf(amax[w], fabsf(x[w][i]));
-        odd += 0.f * s[w] + 0.f * amax[w];
-      } else {
-        amax16(x[w], amax[w], odd);
-      }
+      float x[16];
+      decode16<FROM>(u[w], from[w], x);
+      amax16(x, amax[w], odd);
     }
   }
   if (!dst.page_ok(page)) return;
+  const bool any_odd = block_max2(amax[0], amax[1], odd, red);
+  if (any_odd) {
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      float x[16];
+      decode16<FROM>(u[w], from[w], x);
+      amax[w] = used ? finite_amax16(x, 0.f) : 0.f;
+    }
+    block_max2(amax[0], amax[1], 0.f, red);
+  }
   const size_t at = dst.page_row(page, h) + (size_t)(slot0 % kPage) * dst.hd + threadIdx.x * 16;
   const size_t sc = dst.scale_at(page, h, slot0 % kPage);
-  const float least[2] = {0.f, 0.f};
-  quantise(x, amax, odd, used, used, least, dst.code, {dst.k + at, dst.v + at}, {dst.ks + sc, dst.vs + sc}, red);
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const float s = block_scale<TO>(amax[w]);
+    if (used) {
+      float x[16];
+      decode16<FROM>(u[w], from[w], x);
+      store_codes<TO>((w ? dst.v : dst.k) + at, x, inverse_scale(s), any_odd);
+    }
+    if (threadIdx.x == 0) (w ? dst.vs : dst.ks)[sc] = s;
+  }
 }
 
 }  // namespace
@@ -412,8 +433,13 @@ bool launch_kv8_append(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStrea
   const int t0 = a.first >> c.tshift, t1 = (a.first + a.rows - 1) >> c.tshift;
   const dim3 grid(t1 - t0 + 1, c.n_kv);
   const int threads = (c.hd / 16) << c.tshift;
-  return launch_kv8(io == 0 ? k_kv8_append<__nv_bfloat16> : io == 1 ? k_kv8_append<__half> : k_kv8_append<float>, grid,
-                    threads, 0, st, 1, c, a);
+  const auto kern = c.code == KV8_INT8 ? (io == 0   ? k_kv8_append<__nv_bfloat16, KV8_INT8>
+                                          : io == 1 ? k_kv8_append<__half, KV8_INT8>
+                                                    : k_kv8_append<float, KV8_INT8>)
+                                       : (io == 0   ? k_kv8_append<__nv_bfloat16, KV8_E4M3>
+                                          : io == 1 ? k_kv8_append<__half, KV8_E4M3>
+                                                    : k_kv8_append<float, KV8_E4M3>);
+  return launch_kv8(kern, grid, threads, 0, st, 1, c, a);
 }
 
 bool launch_kv8_read(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_t st) {
@@ -423,8 +449,13 @@ bool launch_kv8_read(const Kv8View& c, const Kv8RowsArgs& a, int io, cudaStream_
   int run = 16;  // shorter runs where sixteen would leave an SM without eight CTAs
   while (run > 1 && (long long)a.rows / run * 2 * parts < 8 * 152) run /= 2;
   const dim3 grid((a.first + a.rows - 1) / run - a.first / run + 1, 2, parts);
-  return launch_kv8(io == 0 ? k_kv8_read<__nv_bfloat16> : io == 1 ? k_kv8_read<__half> : k_kv8_read<float>, grid, threads,
-                    0, st, 1, c, a, run);
+  const auto kern = c.code == KV8_INT8 ? (io == 0   ? k_kv8_read<__nv_bfloat16, KV8_INT8>
+                                          : io == 1 ? k_kv8_read<__half, KV8_INT8>
+                                                    : k_kv8_read<float, KV8_INT8>)
+                                       : (io == 0   ? k_kv8_read<__nv_bfloat16, KV8_E4M3>
+                                          : io == 1 ? k_kv8_read<__half, KV8_E4M3>
+                                                    : k_kv8_read<float, KV8_E4M3>);
+  return launch_kv8(kern, grid, threads, 0, st, 1, c, a, run);
 }
 
 bool launch_kv8_evict(const Kv8View& src, const Kv8View& dst, const Kv8SelectArgs& a, cudaStream_t st) {
@@ -434,8 +465,10 @@ bool launch_kv8_evict(const Kv8View& src, const Kv8View& dst, const Kv8SelectArg
   const bool reload = cand > nr * kSelThreads * kSelKeys;
   if (!launch_kv8(reload ? k_kv8_select<true> : k_kv8_select<false>, dim3(nr, src.n_kv), kSelThreads, 0, st, nr, a))
     return false;
-  return launch_kv8(src.code == KV8_INT8 ? k_kv8_gather<KV8_INT8> : k_kv8_gather<KV8_E4M3>,
-                    dim3(((a.keep - 1) >> dst.tshift) + 1, src.n_kv), (dst.hd / 16) << dst.tshift, 0, st, 1, src, dst,
+  const auto gather = src.code == KV8_INT8
+                          ? (dst.code == KV8_INT8 ? k_kv8_gather<KV8_INT8, KV8_INT8> : k_kv8_gather<KV8_INT8, KV8_E4M3>)
+                          : (dst.code == KV8_INT8 ? k_kv8_gather<KV8_E4M3, KV8_INT8> : k_kv8_gather<KV8_E4M3, KV8_E4M3>);
+  return launch_kv8(gather, dim3(((a.keep - 1) >> dst.tshift) + 1, src.n_kv), (dst.hd / 16) << dst.tshift, 0, st, 1, src, dst,
                     (const int*)a.index, a.keep);
 }
 

@@ -93,12 +93,10 @@ __device__ __forceinline__ void pair_to_half(uint32_t a, uint32_t b, uint32_t (&
 }
 
 // Values of the four codes of a word under scale s (fp32 products of numbers that are exact in fp16).
-__device__ __forceinline__ void decode4(uint32_t w, float s, int code, float* x) {
+template <int CODE>
+__device__ __forceinline__ void decode4(uint32_t w, float s, float* x) {
   uint32_t h01, h23;
-  if (code == KV8_INT8)
-    codes_to_half<KV8_INT8>(w, h01, h23);
-  else
-    codes_to_half<KV8_E4M3>(w, h01, h23);
+  codes_to_half<CODE>(w, h01, h23);
   const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h01));
   const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h23));
   x[0] = __fmul_rn(a.x, s), x[1] = __fmul_rn(a.y, s), x[2] = __fmul_rn(b.x, s), x[3] = __fmul_rn(b.y, s);
@@ -108,18 +106,18 @@ __device__ __forceinline__ void decode4(uint32_t w, float s, int code, float* x)
 // clamped to the largest one.  NaN becomes 0; the product of an infinity and m > 0 clamps.  ODD: whether x may hold a
 // NaN or an infinity; without one |x m| rounds to qmax at most, since the scale is no smaller than the block's
 // largest magnitude over qmax.
-template <bool ODD>
-__device__ __forceinline__ uint32_t encode4(const float* x, float m, int code) {
+template <int CODE, bool ODD>
+__device__ __forceinline__ uint32_t encode4(const float* x, float m) {
   float y[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     y[i] = __fmul_rn(x[i], m);
     if (ODD) {
-      const float lim = code == KV8_INT8 ? 127.f : 448.f;
+      constexpr float lim = CODE == KV8_INT8 ? 127.f : 448.f;
       y[i] = m > 0.f && x[i] == x[i] ? fminf(lim, fmaxf(-lim, y[i])) : 0.f;
     }
   }
-  if (code == KV8_INT8) {
+  if (CODE == KV8_INT8) {
     // 1.5 2^23 + y: the sum's low byte is y rounded to the nearest integer, ties to even, in two's complement
     uint32_t b[4];
 #pragma unroll
@@ -134,8 +132,9 @@ __device__ __forceinline__ uint32_t encode4(const float* x, float m, int code) {
 
 // Scale of a block whose largest finite magnitude is amax (0 where that is below the smallest normal
 // number, so that its inverse is finite), and the inverse that its codes are taken with.
-__device__ __forceinline__ float block_scale(float amax, int code) {
-  const float s = __fdiv_rn(amax, code == KV8_INT8 ? 127.f : 448.f);
+template <int CODE>
+__device__ __forceinline__ float block_scale(float amax) {
+  const float s = __fdiv_rn(amax, CODE == KV8_INT8 ? 127.f : 448.f);
   return s < 1.17549435e-38f ? 0.f : s;
 }
 __device__ __forceinline__ float inverse_scale(float s) { return s > 0.f ? __frcp_rn(s) : 0.f; }
