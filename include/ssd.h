@@ -497,7 +497,8 @@ ssd_status ssd_attention_noalloc(const ssd_attention_args* args, void* cuda_stre
  * so a value is off by at most s / 2 (int8) or 2^-4 of itself (e4m3 above
  * 2^-6 s).  NaN is stored as 0, an infinity as +-qmax.
  * A block-table entry outside [0, pool_pages) names no page: its slots are
- * seen by nobody, read as zero, and what is appended to them is dropped. */
+ * seen by nobody, read as zero, and what is appended to them is dropped.
+ * n_pages at most 2^24, n_kv_heads and query heads for one at most 4096. */
 typedef struct {
   void* k;
   void* v;
@@ -521,7 +522,10 @@ typedef struct {
  * Blocks that start in this range get a scale of their own.  A block whose
  * first slots lie before `first` keeps them: its scale becomes the larger of
  * its old one and the new rows', and their codes are rounded again when it
- * grows.  Slots of the last block past the new rows hold no token afterwards.
+ * grows: they must hold tokens, or the block's scale be 0 (a cleared cache's)
+ * or not finite.  Slots of the last block past the new rows hold no token
+ * afterwards, so that rows appended again from an earlier slot on (the
+ * accepted ones of a verify pass) replace what a rejected draft left.
  * Errors: INVALID_ARG (bad descriptor, alignment or stride; rows < 1; a slot
  * past the block table). */
 ssd_status ssd_kv8_append(const ssd_kv8_cache* cache, const ssd_kv8_rows* rows, void* cuda_stream);
@@ -542,7 +546,9 @@ ssd_status ssd_kv8_read(const ssd_kv8_cache* cache, const ssd_kv8_rows* rows, vo
  * Sums and softmax statistics are fp32; an fp32 q is not rounded below 22
  * bits.  A row that sees no slot gets zeros and lse -inf; slots that a row
  * does not see may hold anything, those past every row's sight need never
- * have been written.  Errors: INVALID_ARG (bad descriptor, pointer,
+ * have been written.  A bounded device-side wait that gives up (see
+ * SSD_ERR_TIMEOUT) is not reported: the output is then incomplete.
+ * Errors: INVALID_ARG (bad descriptor, pointer,
  * alignment or stride, rows not in 1..64, n_q_heads not a multiple of
  * n_kv_heads, a slot past the block table, scale or softcap out of range);
  * CAPACITY (scratch too small). */
@@ -587,8 +593,8 @@ ssd_status ssd_kv8_weights(const ssd_kv8_cache* cache, const ssd_kv8_attention_a
  *   kept_weight  device fp32 [n_kv_heads][keep] or NULL: receives their weights
  * `to` has the heads of `from` (its dtype and block_tokens may differ), and
  * its first ceil(keep / 64) pages must be none of from's.  Errors:
- * INVALID_ARG (bad descriptor or pointer, shapes that differ, not
- * 0 <= recent <= keep <= n, keep < 1, n past the block table); CAPACITY
+ * INVALID_ARG (bad descriptor or pointer, shapes that differ, a layer onto
+ * itself, not 0 <= recent <= keep <= n, keep < 1, n past the block table); CAPACITY
  * (keep past to's block table). */
 typedef struct {
   const float* weight;

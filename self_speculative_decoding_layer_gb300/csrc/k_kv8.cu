@@ -126,6 +126,9 @@ __global__ void __launch_bounds__(kQuantThreads, 2) k_kv8_append(Kv8View c, Kv8R
   if (slot0 < a.first) {  // slots before the new rows stay, under a scale no smaller than theirs
     least[0] = c.ks[sc];
     least[1] = c.vs[sc];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+      if (!(least[w] < INFINITY)) least[w] = 0.f;  // what stands in a block that was never written
     if (row < 0) {
       float unused = 0.f;
       decode16<CODE>(*reinterpret_cast<const uint4*>(c.k + at), least[0], x[0]);

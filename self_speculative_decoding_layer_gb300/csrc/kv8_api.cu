@@ -1,6 +1,5 @@
 // The 8-bit KV cache's entry points: argument checks, then the kernels of
 // k_kv8.cu and k_kv8_attn.cu on the caller's stream.
-#include <limits.h>
 #include <math.h>
 
 #include "../../include/ssd.h"
@@ -9,6 +8,9 @@
 using namespace ssd;
 
 namespace {
+
+constexpr int kMaxPages = 1 << 24;  // of a block table: slot numbers and the tiles past them stay far inside an int
+constexpr int kMaxHeads = 4096;     // KV heads, and query heads of one: grids stay inside their limits
 
 size_t io_size(int dtype) { return dtype == SSD_F32 ? 4 : 2; }
 bool io_ok(int dtype) { return dtype == SSD_BF16 || dtype == SSD_FP16 || dtype == SSD_F32; }
@@ -19,8 +21,8 @@ bool view_of(const ssd_kv8_cache* c, Kv8View* v) {
   if (!c || !aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
       !aligned(c->block_table, 4))
     return false;
-  if (c->n_pages < 1 || c->n_pages > INT_MAX / kPage || c->pool_pages < 1 || c->layer < 0) return false;
-  if (c->n_kv_heads < 1 || c->n_kv_heads > 65535 || (c->head_dim != 64 && c->head_dim != 128)) return false;
+  if (c->n_pages < 1 || c->n_pages > kMaxPages || c->pool_pages < 1 || c->layer < 0) return false;
+  if (c->n_kv_heads < 1 || c->n_kv_heads > kMaxHeads || (c->head_dim != 64 && c->head_dim != 128)) return false;
   if (c->dtype != SSD_I8 && c->dtype != SSD_E4M3) return false;
   if (c->block_tokens != 16 && c->block_tokens != 32 && c->block_tokens != 64) return false;
   const size_t heads = (size_t)c->layer * c->pool_pages * c->n_kv_heads;  // (page, head) units before this layer
@@ -39,7 +41,7 @@ bool view_of(const ssd_kv8_cache* c, Kv8View* v) {
 
 // A matrix of `rows` rows of `width` elements, `ld` apart, that 16-byte accesses can read.
 bool rows_ok(const void* p, int64_t ld, int64_t width, int dtype) {
-  return aligned(p, 16) && ld >= width && (ld * (int64_t)io_size(dtype)) % 16 == 0;
+  return aligned(p, 16) && ld >= width && ld <= (int64_t)1 << 40 && (ld * (int64_t)io_size(dtype)) % 16 == 0;
 }
 
 bool rows_args(const ssd_kv8_cache* c, const ssd_kv8_rows* r, Kv8View* v, Kv8RowsArgs* a) {
@@ -60,12 +62,13 @@ bool rows_args(const ssd_kv8_cache* c, const ssd_kv8_rows* r, Kv8View* v, Kv8Row
 bool attn_args(const ssd_kv8_cache* c, const ssd_kv8_attention_args* p, Kv8AttnArgs* a) {
   if (!view_of(c, &a->c) || !p || !io_ok(p->dtype)) return false;
   if (p->rows < 1 || p->rows > kMaxRows || p->prefix < 0 || p->base < 0) return false;
-  if (p->n_q_heads < 1 || p->n_q_heads % c->n_kv_heads || p->n_q_heads / c->n_kv_heads > 65535) return false;
+  if (p->n_q_heads < 1 || p->n_q_heads % c->n_kv_heads || p->n_q_heads / c->n_kv_heads > kMaxHeads) return false;
   const int64_t slots = (int64_t)c->n_pages * kPage;
   if (p->prefix > slots || (int64_t)p->base + p->rows > slots) return false;
   if (!rows_ok(p->q, p->ld_q, (int64_t)p->n_q_heads * c->head_dim, p->dtype)) return false;
   if (p->lse && !aligned(p->lse, 4)) return false;
   if (!(p->scale > 0.f) || !isfinite(p->scale) || !(p->softcap >= 0.f) || !isfinite(p->softcap)) return false;
+  if (p->softcap > 0.f && p->softcap < 1e-30f) return false;  // (its inverse has to be a number)
   a->q = p->q;
   a->ld_q = (size_t)p->ld_q;
   a->lse = p->lse;
@@ -161,6 +164,7 @@ ssd_status ssd_kv8_evict(const ssd_kv8_cache* from, const ssd_kv8_cache* to, con
   if (p->n < 1 || (int64_t)p->n > (int64_t)from->n_pages * kPage || p->keep < 1 || p->keep > p->n || p->recent < 0 ||
       p->recent > p->keep || p->ld_weight < p->n)
     return SSD_ERR_INVALID_ARG;
+  if (src.k == dst.k && src.btab == dst.btab) return SSD_ERR_INVALID_ARG;  // onto itself
   if ((int64_t)p->keep > (int64_t)to->n_pages * kPage) return SSD_ERR_CAPACITY;
   Kv8SelectArgs a{};
   a.weight = p->weight;

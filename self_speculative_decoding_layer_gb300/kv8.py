@@ -1,7 +1,7 @@
 """KVCache8: one paged 8-bit KV cache and the operators over it (ssd_kv8_* of the C ABI).
 
 Every call works on one layer, runs on the current torch stream of the cache's device and returns without waiting;
-tensors it returns are new (unless given) and belong to that stream.  Arguments are checked and the library called by
+tensors it returns are new (unless given) and belong to that stream.  No gradients are recorded.  Arguments are checked and the library called by
 lib/_kv8.so (csrc/py/kv8_ext.cpp); what it refuses is raised as SSDError.
 """
 from __future__ import annotations
@@ -106,8 +106,8 @@ class KVCache8:
     def weights(self, layer: int, q, lse, prefix: int, base: Optional[int] = None, masks: Optional[Sequence[int]] = None,
                 scale: Optional[float] = None, softcap: float = 0.0, rows: Optional[Sequence[int]] = None, weight=None,
                 out=None):
-        """Add the attention weight that every slot drew from the given rows (None: all) of an attention call, whose
-        arguments are repeated here with the lse it returned, to weight [n_kv_heads, slots] (fp32; None: zeros).
+        """Add the attention weight that every slot drew from the given rows (None: all; each counts once) of an attention
+        call, whose arguments are repeated here with the lse it returned, to weight [n_kv_heads, slots] (fp32; None: zeros).
         Written to out, else into weight, else to a new tensor, which is returned; only its first
         max(prefix, base + rows) columns are touched."""
         return _ext.weights(self._c, layer, q, prefix, base, masks, scale, softcap, lse, rows, weight, out)

@@ -274,6 +274,18 @@ def test_a_nan_query_stays_in_its_row():
     assert torch.equal(out, clean)
 
 
+def test_a_nan_query_stays_in_its_row_on_tcgen05():
+    case = (16, 6272, 0, "causal", 64, 8, 64, "e4m3", 32, "bf16", 0.0)
+    p, q, m, vis, n, base = attention_case(case)
+    clean = p.gpu.attention(1, q.cuda(), 6272)
+    q[3, 9, 7] = float("nan")
+    q[12, 60, 0] = float("inf")
+    out = p.gpu.attention(1, q.cuda(), 6272)
+    assert out[3, 9].isnan().all() and not out[12, 60].isfinite().all()
+    out[3, 9], out[12, 60] = clean[3, 9], clean[12, 60]
+    assert torch.equal(out, clean)
+
+
 def test_large_and_small_queries_keep_their_precision():
     """q rows of very different size: each is scaled by its own power of two."""
     rng = np.random.default_rng(2)
@@ -339,6 +351,85 @@ def test_block_table_entries_outside_the_pool():
     out, lse = p.gpu.attention(1, q.cuda(), 256, 0, masks=[0] * 3, return_lse=True)
     assert not out.any() and torch.isneginf(lse).all()
     p.gpu.block_table.copy_(good)
+
+
+def test_block_table_entries_outside_the_pool_on_tcgen05():
+    rng = np.random.default_rng(16)
+    p = Pair(6400, 8, 64, "int8", 32)
+    p.fill(rng, 6400)
+    q = kc.make_rows(rng, 16, 64, 64, "fp32")
+    keep = np.ones(6400, dtype=bool)
+    for page, entry in ((0, -1), (17, p.gpu.pool_pages), (50, 2 ** 31 - 1), (51, -2 ** 31), (99, p.gpu.pool_pages + 5)):
+        p.gpu.block_table[page] = entry
+        keep[page * 64:page * 64 + 64] = False
+    vis = np.tile(keep, (16, 1))
+    k, v = p.k.values(np.arange(6400)), p.v.values(np.arange(6400))
+    want, _ = kv8.attention(q.numpy(), k, v, vis, 0.125)
+    got = p.gpu.attention(1, q.cuda(), 6400, 0, masks=[0] * 16).cpu().numpy()
+    assert (np.abs(got - want) <= kc.out_error(q.numpy(), k, v, vis, want, 0.125, 0.0, "fp32")).all()
+
+
+def test_offsets_past_32_bits():
+    """Pages and layers that lie past 4 GB of codes: append, read, attention on both kernels, weights, eviction."""
+    import self_speculative_decoding_layer_gb300 as ssd
+
+    heads, hd, pool, layers = 8, 128, 40000, 2  # 2.6 GB of codes a layer and tensor
+    k, v = (torch.empty((layers, pool, heads, 64, hd), dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((layers, pool, heads, 2), device="cuda") for _ in range(2))
+    pages = 100
+    perm = np.random.default_rng(3).permutation(np.arange(pool - 120, pool))
+    c = ssd.KVCache8.wrap(k, v, ks, vs, torch.tensor(perm[:pages], dtype=torch.int32, device="cuda"))
+    d = ssd.KVCache8.wrap(k, v, ks, vs, torch.tensor(perm[pages:], dtype=torch.int32, device="cuda"))
+    p = Pair(pages * 64, heads, hd, "int8", 32, layers=1, layer=0)
+    rng = np.random.default_rng(5)
+    n = pages * 64
+    x, y = kc.make_rows(rng, n, heads, hd, "bf16").cuda(), kc.make_rows(rng, n, heads, hd, "bf16").cuda()
+    c.append(1, x, y, 0)
+    p.gpu.append(0, x, y, 0)
+    for a, b in zip(c.read(1, 0, n), p.gpu.read(0, 0, n)):
+        assert torch.equal(a, b)
+    for rows in (1, 16):
+        q = kc.make_rows(rng, rows, 64, hd, "bf16").cuda()
+        (o, lse), (o2, lse2) = (g.attention(i, q, n - rows, return_lse=True) for g, i in ((c, 1), (p.gpu, 0)))
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        w, w2 = c.weights(1, q, lse, n - rows), p.gpu.weights(0, q, lse, n - rows)
+        assert torch.equal(w, w2)
+    index, _ = c.evict(1, w, 1000, 10, d, 1)
+    e = ssd.KVCache8(1, heads, hd, 1000, block_tokens=32)
+    index2, _ = p.gpu.evict(0, w, 1000, 10, e, 0)
+    assert torch.equal(index, index2)
+    for a, b in zip(d.read(1, 0, 1000), e.read(0, 0, 1000)):
+        assert torch.equal(a, b)
+
+
+def test_two_attentions_at_once():
+    """Calls on two streams with no order between them, on both kernels, over and over: no result depends on the other."""
+    rng = np.random.default_rng(17)
+    p = Pair(6400, 8, 64, "int8", 32)
+    p.fill(rng, 6400)
+    qs = [kc.make_rows(rng, r, 64, 64, "fp32").cuda() for r in (1, 16, 16, 3)]
+    want = [p.gpu.attention(1, q, 6400 - q.shape[0]) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    got = []
+    for rep in range(30):
+        for q, s in zip(qs, streams):
+            with torch.cuda.stream(s):
+                got.append((q, p.gpu.attention(1, q, 6400 - q.shape[0])))
+    torch.cuda.synchronize()
+    for i, (q, o) in enumerate(got):
+        assert torch.equal(o, want[i % 4]), i
+
+
+def test_output_over_the_queries():
+    rng = np.random.default_rng(18)
+    p = Pair(6400, 8, 64, "int8", 32)
+    p.fill(rng, 6400)
+    for rows, prefix in ((1, 300), (3, 6000), (16, 6300)):
+        q = kc.make_rows(rng, rows, 64, 64, "fp32").cuda()
+        want = p.gpu.attention(1, q, prefix)
+        assert p.gpu.attention(1, q, prefix, out=q) is q
+        assert torch.equal(q, want)
 
 
 # ---------------------------------------------------------------- eviction
@@ -533,7 +624,9 @@ def test_binding_refusals():
         lambda: c.weights(1, q, lse, 10, weight=w[:1].expand(4, 128)), lambda: c.weights(1, q, lse, 10, weight=w, out=w[:, :64].contiguous()),
         lambda: c.evict(1, w, 65, 0, d, 1), lambda: c.evict(1, w, 0, 0, d, 1), lambda: c.evict(1, w, 8, 9, d, 1),
         lambda: c.evict(1, w[:2], 8, 0, d, 1), lambda: c.evict(1, w, 8, 0, Pair(64, 2, 64, "int8", 16).gpu, 1),
-        lambda: c.evict(1, torch.zeros((4, 129), device="cuda"), 8, 0, d, 1),
+        lambda: c.evict(1, torch.zeros((4, 129), device="cuda"), 8, 0, d, 1), lambda: c.evict(1, w, 8, 0, c, 1),
+        lambda: c.attention(1, q.expand(2, 8, 64)[:1].expand(2, 8, 64), 10), lambda: c.append(1, ok, None, 0),
+        lambda: c.append(1, ok, ok, 2 ** 40), lambda: c.attention(1, q, 10, softcap=1e-35),
         lambda: ssd.KVCache8(1, 4, 96, 100), lambda: ssd.KVCache8(1, 4, 64, 0), lambda: ssd.KVCache8(1, 4, 64, 64, dtype=torch.uint8),
         lambda: ssd.KVCache8(1, 4, 64, 64, block_tokens=8), lambda: ssd.KVCache8.wrap(g.k, g.v[:1], g.k_scale, g.v_scale, g.block_table),
         lambda: ssd.KVCache8.wrap(g.k, g.v, g.k_scale[..., :3], g.v_scale, g.block_table),

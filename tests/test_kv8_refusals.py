@@ -50,7 +50,7 @@ def evict(**kw):
 
 BAD_CACHE = [dict(k=None), dict(v=None), dict(k_scale=None), dict(v_scale=None), dict(block_table=None), dict(k=A + 8),
              dict(v=A + 1), dict(k_scale=A + 2), dict(block_table=A + 1), dict(n_pages=0), dict(n_pages=-1),
-             dict(n_pages=2 ** 25), dict(pool_pages=0), dict(layer=-1), dict(n_kv_heads=0), dict(n_kv_heads=65536),
+             dict(n_pages=2 ** 24 + 1), dict(pool_pages=0), dict(layer=-1), dict(n_kv_heads=0), dict(n_kv_heads=4097),
              dict(head_dim=96), dict(head_dim=256), dict(dtype=0), dict(dtype=2), dict(dtype=5), dict(block_tokens=8),
              dict(block_tokens=128), dict(block_tokens=0)]
 
@@ -64,8 +64,8 @@ def test_bad_descriptors(lib, bad):
     assert lib.ssd_kv8_attention_scratch_bytes(ctypes.byref(c), ctypes.byref(a)) == 0
     assert lib.ssd_kv8_attention(ctypes.byref(c), ctypes.byref(a), A, 1 << 30, None) == INVALID
     assert lib.ssd_kv8_weights(ctypes.byref(c), ctypes.byref(a), 1, A, A, 256, None) == INVALID
-    assert lib.ssd_kv8_evict(ctypes.byref(c), ctypes.byref(cache()), ctypes.byref(e), None) == INVALID
-    assert lib.ssd_kv8_evict(ctypes.byref(cache()), ctypes.byref(c), ctypes.byref(e), None) == INVALID
+    assert lib.ssd_kv8_evict(ctypes.byref(c), ctypes.byref(cache(block_table=2 * A)), ctypes.byref(e), None) == INVALID
+    assert lib.ssd_kv8_evict(ctypes.byref(cache(block_table=2 * A)), ctypes.byref(c), ctypes.byref(e), None) == INVALID
 
 
 @pytest.mark.parametrize("bad", [dict(k=None), dict(v=A + 4), dict(ld_k=1023), dict(ld_v=1026), dict(dtype=3), dict(dtype=-1),
@@ -78,9 +78,9 @@ def test_bad_rows(lib, bad):
 
 
 BAD_ATTN = [dict(q=None), dict(q=A + 4), dict(ld_q=4095), dict(ld_q=4097), dict(dtype=3), dict(n_q_heads=12),
-            dict(n_q_heads=0), dict(rows=0), dict(rows=65), dict(prefix=-1), dict(prefix=257), dict(base=-1), dict(base=256),
+            dict(n_q_heads=0), dict(n_q_heads=8 * 4097, ld_q=8 * 4097 * 128), dict(ld_q=2 ** 62), dict(rows=0), dict(rows=65), dict(prefix=-1), dict(prefix=257), dict(base=-1), dict(base=256),
             dict(base=2 ** 31 - 1), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan),
-            dict(softcap=-1.0), dict(softcap=math.inf), dict(softcap=math.nan), dict(lse=A + 2)]
+            dict(softcap=-1.0), dict(softcap=1e-35), dict(softcap=math.inf), dict(softcap=math.nan), dict(lse=A + 2)]
 
 
 @pytest.mark.parametrize("bad", BAD_ATTN, ids=str)
@@ -116,12 +116,14 @@ def test_bad_outputs_and_scratch(lib):
                                  dict(n=257, ld_weight=300), dict(keep=0), dict(keep=257), dict(recent=-1), dict(recent=65),
                                  dict(ld_weight=255)], ids=str)
 def test_bad_evictions(lib, bad):
-    assert lib.ssd_kv8_evict(ctypes.byref(cache()), ctypes.byref(cache()), ctypes.byref(evict(**bad)), None) == INVALID
+    assert lib.ssd_kv8_evict(ctypes.byref(cache()), ctypes.byref(cache(layer=1)), ctypes.byref(evict(**bad)), None) == INVALID
 
 
 def test_evictions_between_caches_that_differ(lib):
     e = evict()
-    for other, rc in ((cache(n_kv_heads=4), INVALID), (cache(head_dim=64), INVALID), (cache(n_pages=1), 0)):
+    # onto itself
+    assert lib.ssd_kv8_evict(ctypes.byref(cache(layer=1)), ctypes.byref(cache(layer=1)), ctypes.byref(e), None) == INVALID
+    for other, rc in ((cache(n_kv_heads=4), INVALID), (cache(head_dim=64), INVALID), (cache(layer=1, n_pages=1), 0)):
         e.keep = 65 if rc == 0 else 64
         assert lib.ssd_kv8_evict(ctypes.byref(cache()), ctypes.byref(other), ctypes.byref(e), None) == (rc or CAPACITY)
 
