@@ -202,6 +202,7 @@ constexpr int kSelCluster = 8;
 constexpr int kSelKeys = 8;      // keys that a thread holds in registers
 constexpr int kDigitBits = 11;   // 32 bits in rounds of 11, 11 and 10
 constexpr int kBins = 1 << kDigitBits;
+constexpr int kCoarse = kBins / kSelWarps;  // 64
 
 // A key that orders weights as unsigned integers: larger weight, larger key; -0 and +0 alike; NaN below all.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -234,15 +235,17 @@ __device__ __forceinline__ int warps_before(int v, int* sums, int& total) {
 
 // Grid (cluster CTAs, heads).  The keep - recent heaviest of slots [0, n - recent), the lowest slots among equal ones,
 // in slot order, then the recent ones.  A radix select: three rounds of a shared-memory histogram of the next digit
-// over the keys that still agree with the threshold, added up over the cluster.  A thread holds its consecutive keys
+// over the keys that still agree with the threshold, added up over the cluster.  Of the other CTAs' histograms only the
+// sums of 64 bins each and then the 64 bins of one sum are read (all of them: 64 KB a CTA and round, 2.5 us).  A thread holds its consecutive keys
 // in registers (RELOAD: more than fit are read again each round).
 template <bool RELOAD>
 __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
   namespace cg = cooperative_groups;
   __shared__ int hist[2][kBins];
+  __shared__ int coarse[2][kSelWarps];          // sums of kCoarse bins
   __shared__ int sums[kSelWarps];
-  __shared__ int s_bin, s_above;
-  __shared__ int s_count[2];  // this CTA's candidates above / equal to the threshold
+  __shared__ int s_bin, s_above, s_part, s_part_above;
+  __shared__ int2 s_count[kSelCluster];         // each rank's candidates above / equal to the threshold
   cg::cluster_group cl = cg::this_cluster();
   const int rank = cl.block_rank(), nr = cl.num_blocks();
   const int h = blockIdx.y, tid = threadIdx.x;
@@ -263,12 +266,20 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
   const int span = (cand + nr - 1) / nr;
   const int i0 = min(cand, rank * span), i1 = min(cand, i0 + span);
   const int mine = i0 + (tid >> 5) * 32 * kSelKeys + (tid & 31);
-  float x[kSelKeys];
+  uint32_t key[kSelKeys];  // made once, since the rounds' arithmetic over eight keys a thread is what bounds the kernel
+  uint32_t valid = 0;      // bit e: key e is a candidate's
   auto load = [&](int run) {
+    float x[kSelKeys];
+    valid = 0;
 #pragma unroll
-    for (int e = 0; e < kSelKeys; ++e) x[e] = mine + run + e * 32 < i1 ? __ldg(w + mine + run + e * 32) : 0.f;
+    for (int e = 0; e < kSelKeys; ++e) {
+      const bool v = mine + run + e * 32 < i1;
+      x[e] = v ? __ldg(w + mine + run + e * 32) : 0.f;
+      valid |= (uint32_t)v << e;
+    }
+#pragma unroll
+    for (int e = 0; e < kSelKeys; ++e) key[e] = weight_key(x[e]);
   };
-  auto valid = [&](int run, int e) { return mine + run + e * 32 < i1; };
   const int n_run = RELOAD ? (i1 - i0 + RUN - 1) / RUN * RUN : RUN;
   if (!RELOAD) load(0);
   uint32_t prefix = 0;  // the threshold's leading bits found so far
@@ -281,32 +292,49 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
     __syncthreads();
     for (int run = 0; run < n_run; run += RUN) {
       if (RELOAD) load(run);
+      const uint32_t digit = (1u << bits) - 1;
 #pragma unroll
-      for (int e = 0; e < kSelKeys; ++e) {
-        const uint32_t k = weight_key(x[e]);
-        if (valid(run, e) && (round == 0 || (k >> (shift + bits)) == prefix)) atomicAdd(&hs[(k >> shift) & ((1u << bits) - 1)], 1);
-      }
+      for (int e = 0; e < kSelKeys; ++e)
+        if ((valid >> e & 1u) && (round == 0 || (key[e] >> (shift + bits)) == prefix)) atomicAdd(&hs[(key[e] >> shift) & digit], 1);
+    }
+    __syncthreads();
+    {
+      const int2 t = *reinterpret_cast<const int2*>(hs + 2 * tid);  // warp w's lanes hold coarse bin w
+      const int c = __reduce_add_sync(0xffffffffu, t.x + t.y);
+      if ((tid & 31) == 0) coarse[round & 1][tid >> 5] = c;
     }
     cl.sync();
-    // two bins a thread, from the top one down; the bin where the count from the top reaches need
-    int v[2] = {0, 0};
+    if (tid < 32) {  // the coarse bin, from the top one down, where the count reaches need
+      int v = 0;
 #pragma unroll
-    for (int r = 0; r < kSelCluster; ++r)
-      if (r < nr) {
-        const int2 t = *reinterpret_cast<const int2*>(cl.map_shared_rank(hs, r) + kBins - 2 - 2 * tid);
-        v[0] += t.y;
-        v[1] += t.x;
+      for (int r = 0; r < kSelCluster; ++r)
+        if (r < nr) v += cl.map_shared_rank(coarse[round & 1], r)[31 - tid];
+      const int above = warp_prefix(v) - v;
+      if (above < need && above + v >= need) {
+        s_part = 31 - tid;
+        s_part_above = above;
       }
-    int total;
-    const int inc = warp_prefix(v[0] + v[1]);
-    int above = warps_before(__shfl_sync(0xffffffffu, inc, 31), sums, total) + inc - v[0] - v[1];
+      __syncwarp();
+      // and the bin among its 64, two a lane
+      const int top = s_part * kCoarse + kCoarse - 2 - 2 * tid;
+      int2 u = make_int2(0, 0);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (above < need && above + v[e] >= need) {
-        s_bin = kBins - 1 - 2 * tid - e;
-        s_above = above;
+      for (int r = 0; r < kSelCluster; ++r)
+        if (r < nr) {
+          const int2 t = *reinterpret_cast<const int2*>(cl.map_shared_rank(hs, r) + top);
+          u.x += t.x;
+          u.y += t.y;
+        }
+      int at = s_part_above + warp_prefix(u.x + u.y) - u.x - u.y;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int n = e ? u.x : u.y;
+        if (at < need && at + n >= need) {
+          s_bin = top + 1 - e;
+          s_above = at;
+        }
+        at += n;
       }
-      above += v[e];
     }
     __syncthreads();
     prefix = (prefix << bits) | (uint32_t)s_bin;
@@ -315,52 +343,50 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
   }
   // prefix is the threshold's key; candidates above it are taken, and the first `need` equal ones.
   int gt = 0, eq = 0;  // of this warp
-  auto count = [&](int run) {
+  auto count = [&]() {
     gt = eq = 0;
 #pragma unroll
     for (int e = 0; e < kSelKeys; ++e) {
-      const uint32_t k = weight_key(x[e]);
-      gt += __popc(__ballot_sync(0xffffffffu, valid(run, e) && k > prefix));
-      eq += __popc(__ballot_sync(0xffffffffu, valid(run, e) && k == prefix));
+      gt += __popc(__ballot_sync(0xffffffffu, (valid >> e & 1u) && key[e] > prefix));
+      eq += __popc(__ballot_sync(0xffffffffu, (valid >> e & 1u) && key[e] == prefix));
     }
   };
-  if (tid < 2) s_count[tid] = 0;
-  __syncthreads();
+  int cta_gt = 0, cta_eq = 0;
   for (int run = 0; run < n_run; run += RUN) {
     if (RELOAD) load(run);
-    count(run);
-    if ((tid & 31) == 0) {
-      atomicAdd(&s_count[0], gt);
-      atomicAdd(&s_count[1], eq);
-    }
+    count();
+    int tg, te;
+    warps_before(gt, sums, tg);
+    warps_before(eq, sums, te);
+    cta_gt += tg;
+    cta_eq += te;
   }
-  cl.sync();
+  if (tid < nr) cl.map_shared_rank(s_count, tid)[rank] = make_int2(cta_gt, cta_eq);
+  cl.sync();  // (no CTA's shared memory is read by another after this)
   int base_gt = 0, base_eq = 0;  // in the CTAs before this one
 #pragma unroll
   for (int r = 0; r < kSelCluster; ++r)
     if (r < rank) {
-      const int* c = cl.map_shared_rank(s_count, r);
-      base_gt += c[0];
-      base_eq += c[1];
+      base_gt += s_count[r].x;
+      base_eq += s_count[r].y;
     }
   for (int run = 0; run < n_run; run += RUN) {
     if (RELOAD) {
       load(run);
-      count(run);
+      count();
     }
     int tg, te;
     int ng = base_gt + warps_before(gt, sums, tg), ne = base_eq + warps_before(eq, sums, te);
     const unsigned below = (1u << (tid & 31)) - 1;
 #pragma unroll
     for (int e = 0; e < kSelKeys; ++e) {
-      const uint32_t k = weight_key(x[e]);
-      const bool g = valid(run, e) && k > prefix, q = valid(run, e) && k == prefix;
+      const bool g = (valid >> e & 1u) && key[e] > prefix, q = (valid >> e & 1u) && key[e] == prefix;
       const unsigned bg = __ballot_sync(0xffffffffu, g), bq = __ballot_sync(0xffffffffu, q);
       const int eq_before = ne + __popc(bq & below);
       if (g || (q && eq_before < need)) {
         const int pos = ng + __popc(bg & below) + min(eq_before, need);
         index[pos] = mine + run + e * 32;
-        if (kept) kept[pos] = x[e];
+        if (kept) kept[pos] = __ldg(w + mine + run + e * 32);  // (as it stands there, NaN and -0 among them)
       }
       ng += __popc(bg);
       ne += __popc(bq);
@@ -368,7 +394,6 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
     base_gt += tg;
     base_eq += te;
   }
-  cl.sync();  // no CTA leaves while another may read its counters
 }
 
 // Grid (blocks of the kept slots, heads).  A thread keeps its two chunks as codes, not values, over the reduction: a
