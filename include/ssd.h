@@ -540,7 +540,8 @@ ssd_status ssd_kv8_read(const ssd_kv8_cache* cache, const ssd_kv8_rows* rows, vo
  * h / (n_q_heads / n_kv_heads).
  *   q    device [rows][n_q_heads * head_dim], RoPE applied, ld_q elements apart
  *   out  device, the same shape, ld_out apart
- *   lse  device fp32 [rows][n_q_heads] or NULL: the log of the sum of exp of each row's scores
+ *   lse  device fp32 [rows][n_q_heads] or NULL: the log of the sum of exp of each row's scores;
+ *        ld_lse and step_lse elements between rows and between heads (both 0: n_q_heads and 1)
  *   dtype of q and out: SSD_F32, SSD_BF16 or SSD_FP16; 16-byte aligned, rows a multiple of 16 bytes apart
  *   scores are scale * q.k (scale > 0), with softcap > 0 then softcap * tanh(score / softcap)
  * Sums and softmax statistics are fp32; an fp32 q is not rounded below 22
@@ -556,7 +557,7 @@ typedef struct {
   const void* q;
   void* out;
   float* lse;
-  int64_t ld_q, ld_out;
+  int64_t ld_q, ld_out, ld_lse, step_lse;
   int dtype, n_q_heads, rows, prefix, base;
   float scale, softcap;
   uint64_t mask[64];

@@ -92,8 +92,8 @@ class KV8RowsC(ctypes.Structure):
 
 class KV8AttentionArgsC(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("ld_q", ctypes.c_int64),
-                ("ld_out", ctypes.c_int64), ("dtype", ctypes.c_int), ("n_q_heads", ctypes.c_int),
-                ("rows", ctypes.c_int), ("prefix", ctypes.c_int), ("base", ctypes.c_int), ("scale", ctypes.c_float),
+                ("ld_out", ctypes.c_int64), ("ld_lse", ctypes.c_int64), ("step_lse", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("n_q_heads", ctypes.c_int), ("rows", ctypes.c_int), ("prefix", ctypes.c_int), ("base", ctypes.c_int), ("scale", ctypes.c_float),
                 ("softcap", ctypes.c_float), ("mask", ctypes.c_uint64 * 64)]
 
 

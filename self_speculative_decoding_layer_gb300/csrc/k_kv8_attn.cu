@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(
     const float f = sum == 0.f ? 0.f : 1.f / sum;
     store4(reinterpret_cast<T*>(a.out) + (size_t)r * a.ld_out + (size_t)head * HD + d,
            make_float4(x.x * f, x.y * f, x.z * f, x.w * f));
-    if (d == 0 && a.lse) a.lse[(size_t)r * a.n_q + head] = lse_of(M, sum);
+    if (d == 0 && a.lse) a.lse[a.lse_at(r, head)] = lse_of(M, sum);
   };
 
   __syncthreads();
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(HD) k_kv8_merge(const __grid_constant__ Kv8Att
     *out = y;
   else
     *out = Io<T>::from_f(y);
-  if (threadIdx.x == 0 && a.lse) a.lse[(size_t)r * a.n_q + head] = lse_of(M, sum);
+  if (threadIdx.x == 0 && a.lse) a.lse[a.lse_at(r, head)] = lse_of(M, sum);
 }
 
 // ---------------------------------------------------------------- accumulated weights
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
       if (qi < nq) {
         const int ti = qi / a.group, r = a.take[ti], head = h * a.group + qi - ti * a.group;
         p = reinterpret_cast<const T*>(a.q) + (size_t)r * a.ld_q + (size_t)head * HD;
-        lse = __ldg(a.lse + (size_t)r * a.n_q + head);
+        lse = __ldg(a.lse + a.lse_at(r, head));
         mask = a.mask[r];
       }
       const float inv = stage_query<T, HD, SPLIT>(p, s_hi + (q >> 3) * QW, s_lo + (q >> 3) * QW, q & 7, lane);

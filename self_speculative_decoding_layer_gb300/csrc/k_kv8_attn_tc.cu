@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
         if (a.part_o)
           a.part_ml[at] = make_float2(top, l);
         else if (a.lse)
-          a.lse[(size_t)r * a.n_q + head] = lse_of(top, l);
+          a.lse[a.lse_at(r, head)] = lse_of(top, l);
       }
     }
   }

@@ -51,8 +51,8 @@ struct Kv8AttnArgs {
   Kv8View c;
   const void* q;    // [rows][ld_q], query heads of hd
   void* out;        // [rows][ld_out]
-  float* lse;       // [rows][n_q] or null; the weights kernel reads it
-  size_t ld_q, ld_out;
+  float* lse;       // [rows][n_q] or null, ld_lse and step_lse apart; the weights kernel reads it
+  size_t ld_q, ld_out, ld_lse, step_lse;
   int n_q, group, rows;
   int prefix, base;
   float scale, cap;          // cap 0: none
@@ -68,6 +68,8 @@ struct Kv8AttnArgs {
   int n_take;                // query rows that count
   unsigned char take[kMaxRows];
   unsigned long long mask[kMaxRows];
+
+  __device__ __forceinline__ size_t lse_at(int row, int head) const { return row * ld_lse + head * step_lse; }
 };
 
 // io: ssd_dtype of q / out, k / v rows.

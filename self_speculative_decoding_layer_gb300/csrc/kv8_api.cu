@@ -12,6 +12,8 @@ namespace {
 constexpr int kMaxPages = 1 << 24;  // of a block table: slot numbers and the tiles past them stay far inside an int
 constexpr int kMaxHeads = 4096;     // KV heads, and query heads of one: grids stay inside their limits
 
+constexpr int64_t kMaxStride = (int64_t)1 << 40;
+
 size_t io_size(int dtype) { return dtype == SSD_F32 ? 4 : 2; }
 bool io_ok(int dtype) { return dtype == SSD_BF16 || dtype == SSD_FP16 || dtype == SSD_F32; }
 bool aligned(const void* p, size_t a) { return p && ((uintptr_t)p & (a - 1)) == 0; }
@@ -41,7 +43,7 @@ bool view_of(const ssd_kv8_cache* c, Kv8View* v) {
 
 // A matrix of `rows` rows of `width` elements, `ld` apart, that 16-byte accesses can read.
 bool rows_ok(const void* p, int64_t ld, int64_t width, int dtype) {
-  return aligned(p, 16) && ld >= width && ld <= (int64_t)1 << 40 && (ld * (int64_t)io_size(dtype)) % 16 == 0;
+  return aligned(p, 16) && ld >= width && ld <= kMaxStride && (ld * (int64_t)io_size(dtype)) % 16 == 0;
 }
 
 bool rows_args(const ssd_kv8_cache* c, const ssd_kv8_rows* r, Kv8View* v, Kv8RowsArgs* a) {
@@ -72,6 +74,10 @@ bool attn_args(const ssd_kv8_cache* c, const ssd_kv8_attention_args* p, Kv8AttnA
   a->q = p->q;
   a->ld_q = (size_t)p->ld_q;
   a->lse = p->lse;
+  if (p->ld_lse < 0 || p->step_lse < 0 || p->ld_lse > kMaxStride || p->step_lse > kMaxStride) return false;
+  const bool plain = p->ld_lse == 0 && p->step_lse == 0;
+  a->ld_lse = plain ? (size_t)p->n_q_heads : (size_t)p->ld_lse;
+  a->step_lse = plain ? 1 : (size_t)p->step_lse;
   a->n_q = p->n_q_heads;
   a->group = p->n_q_heads / c->n_kv_heads;
   a->rows = p->rows;

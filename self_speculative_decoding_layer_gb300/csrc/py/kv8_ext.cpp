@@ -228,7 +228,7 @@ void attention_args(const Cache& c, PyObject* const* a, ssd_kv8_attention_args* 
   p->q = q.data_ptr();
   p->out = nullptr;
   p->lse = nullptr;
-  p->ld_out = 0;
+  p->ld_out = p->ld_lse = p->step_lse = 0;
   p->dtype = io_of(q.scalar_type());
   p->n_q_heads = (int)q.size(1);
   p->rows = (int)q.size(0);
@@ -318,10 +318,8 @@ PyObject* py_weights(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     ssd_kv8_attention_args p;
     attention_args(c, a + 2, &p);
     const at::Tensor& lse = tensor_of(a[8], "lse");
-    if (lse.dim() != 2 || lse.size(0) != p.rows || lse.size(1) != p.n_q_heads || lse.scalar_type() != at::kFloat ||
-        !lse.is_contiguous() || !here(c, lse))
-      refuse("lse is the contiguous float32 [rows, heads] of the attention call");
-    p.lse = lse.data_ptr<float>();
+    if (lse.dim() != 2 || lse.size(0) != p.rows || lse.size(1) != p.n_q_heads || lse.scalar_type() != at::kFloat || !here(c, lse))
+      refuse("lse is the float32 [rows, heads] of the attention call");
     const int64_t slots = std::max<int64_t>({(int64_t)p.prefix, (int64_t)p.base + p.rows, 1});
     uint64_t take = 0;
     if (a[9] == Py_None) {
@@ -344,6 +342,9 @@ PyObject* py_weights(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
       Py_DECREF(seq);
     }
     const Stream s(c);
+    p.lse = lse.data_ptr<float>();
+    p.ld_lse = lse.stride(0);
+    p.step_lse = lse.stride(1);
     PyObject* result = a[11] != Py_None ? a[11] : a[10];
     at::Tensor out;
     if (result == Py_None) {

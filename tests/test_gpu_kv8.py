@@ -263,6 +263,17 @@ def test_strided_queries_and_outputs():
     assert (room[:, :8] == 7.0).all()
 
 
+def test_weights_take_any_layout_of_lse():
+    case = (5, 333, 0, "causal", 12, 4, 128, "e4m3", 16, "bf16", 0.0)
+    p, q, m, vis, n, base = attention_case(case)
+    _, lse = p.gpu.attention(1, q.cuda(), 333, return_lse=True)
+    want = p.gpu.weights(1, q.cuda(), lse, 333)
+    assert torch.equal(p.gpu.weights(1, q.cuda(), lse.t().contiguous().t(), 333), want)
+    wide = torch.zeros((5, 30), device="cuda")
+    wide[:, 4:28:2] = lse
+    assert torch.equal(p.gpu.weights(1, q.cuda(), wide[:, 4:28:2], 333), want)
+
+
 def test_a_nan_query_stays_in_its_row():
     case = (4, 90, 0, "causal", 8, 2, 64, "int8", 16, "fp32", 0.0)
     p, q, m, vis, n, base = attention_case(case)

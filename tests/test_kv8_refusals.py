@@ -28,7 +28,7 @@ def cache(**kw):
 
 
 def attn(**kw):
-    a = ssd.KV8AttentionArgsC(A, A, A, 4096, 4096, 2, 32, 1, 100, 100, 0.1, 0.0)
+    a = ssd.KV8AttentionArgsC(A, A, A, 4096, 4096, 0, 0, 2, 32, 1, 100, 100, 0.1, 0.0)
     for k, v in kw.items():
         setattr(a, k, v)
     return a
@@ -80,7 +80,8 @@ def test_bad_rows(lib, bad):
 BAD_ATTN = [dict(q=None), dict(q=A + 4), dict(ld_q=4095), dict(ld_q=4097), dict(dtype=3), dict(n_q_heads=12),
             dict(n_q_heads=0), dict(n_q_heads=8 * 4097, ld_q=8 * 4097 * 128), dict(ld_q=2 ** 62), dict(rows=0), dict(rows=65), dict(prefix=-1), dict(prefix=257), dict(base=-1), dict(base=256),
             dict(base=2 ** 31 - 1), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan),
-            dict(softcap=-1.0), dict(softcap=1e-35), dict(softcap=math.inf), dict(softcap=math.nan), dict(lse=A + 2)]
+            dict(softcap=-1.0), dict(softcap=1e-35), dict(softcap=math.inf), dict(softcap=math.nan), dict(lse=A + 2), dict(ld_lse=-1),
+            dict(step_lse=-4), dict(ld_lse=2 ** 50)]
 
 
 @pytest.mark.parametrize("bad", BAD_ATTN, ids=str)
@@ -137,6 +138,12 @@ def test_scratch_covers_every_split(lib):
             got = lib.ssd_kv8_attention_scratch_bytes(
                 ctypes.byref(c), ctypes.byref(attn(rows=n_rows, prefix=prefix, base=prefix)))
             assert 256 <= got <= 152 * 256 * (128 + 2) * 4 + 256, (n_rows, prefix, got)
+
+
+def test_binding_structs_match_the_c_layout(lib):
+    out = (ctypes.c_size_t * 9)()
+    lib.ssd_abi_sizes(out, 9)
+    assert list(out)[5:] == [ctypes.sizeof(c) for c in (ssd.KV8CacheC, ssd.KV8RowsC, ssd.KV8AttentionArgsC, ssd.KV8EvictArgsC)]
 
 
 # ---------------------------------------------------------------- the oracle's definition
