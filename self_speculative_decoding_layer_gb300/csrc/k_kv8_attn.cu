@@ -53,9 +53,8 @@ __device__ __forceinline__ float stage_query(const T* q, uint32_t* hi, uint32_t*
     x[2 * i + 1] = v.y;
     amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
   }
-  amax = warp_max(amax);
   float f, inv;
-  query_factor(amax, f, inv);
+  query_factor(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))), f, inv);  // (amax >= 0)
 #pragma unroll
   for (int i = 0; i < EPL / 2; ++i) {
     const int e = 64 * i + 2 * lane;  // even element of the pair
@@ -646,7 +645,7 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
     load(cur, first, page_of(first));
     int page = page_of(first + stride);
     if (q0) __syncthreads();
-#pragma unroll 4
+#pragma unroll 8
     for (int q = warp; q < eights * 8; q += kWWarps) {
       const int qi = q0 + q;
       const T* p = nullptr;
