@@ -89,20 +89,28 @@ __device__ __forceinline__ void scores(float (&s)[2][QT][4], const uint4 (&klo)[
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
       const uint4 h = *reinterpret_cast<const uint4*>(qhi + t * QW + (p * 32 + lane) * 4);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if (p == 0)
-          mma16816_first(s[b][t], a[0][b], h.x, h.y);
-        else
-          mma16816(s[b][t], a[0][b], h.x, h.y);
-        mma16816(s[b][t], a[1][b], h.z, h.w);
-      }
       if (SPLIT) {
+        // The tensor cores cut off what does not fit an accumulator, so a pair of steps starts from nothing, with its
+        // small part first, and the pairs are added rounded (one chain of all steps was about twice as far off).
         const uint4 l = *reinterpret_cast<const uint4*>(qlo + t * QW + (p * 32 + lane) * 4);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          mma16816(s[b][t], a[0][b], l.x, l.y);
-          mma16816(s[b][t], a[1][b], l.z, l.w);
+          float d[4];
+          mma16816_first(d, a[0][b], l.x, l.y);
+          mma16816(d, a[1][b], l.z, l.w);
+          mma16816(d, a[0][b], h.x, h.y);
+          mma16816(d, a[1][b], h.z, h.w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[b][t][e] = p == 0 ? d[e] : s[b][t][e] + d[e];
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if (p == 0)
+            mma16816_first(s[b][t], a[0][b], h.x, h.y);
+          else
+            mma16816(s[b][t], a[0][b], h.x, h.y);
+          mma16816(s[b][t], a[1][b], h.z, h.w);
         }
       }
     }
@@ -305,7 +313,7 @@ __global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(
 #pragma unroll
         for (int t = 0; t < QT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[b][t][e] = capped(s[b][t][e], a.cap);
+          for (int e = 0; e < 4; ++e) s[b][t][e] = capped<SPLIT>(s[b][t][e], a.cap);
     }
     if (!full) {
       vmax = fmaxf(visible_any(slot0, a) ? head.vs[0] : 0.f, visible_any(slot0 + 16, a) ? head.vs[1] : 0.f);
@@ -709,8 +717,8 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
         const float2 lse = *reinterpret_cast<const float2*>(s_lse + t * 8 + 2 * c);
         const float c0 = cf.x * ks, c1 = cf.y * ks;
         if (CAP) {
-          x[0] = capped((s0[0] + s1[0]) * c0, a.cap) - lse.x, x[1] = capped((s0[1] + s1[1]) * c1, a.cap) - lse.y;
-          x[2] = capped((s0[2] + s1[2]) * c0, a.cap) - lse.x, x[3] = capped((s0[3] + s1[3]) * c1, a.cap) - lse.y;
+          x[0] = capped<SPLIT>((s0[0] + s1[0]) * c0, a.cap) - lse.x, x[1] = capped<SPLIT>((s0[1] + s1[1]) * c1, a.cap) - lse.y;
+          x[2] = capped<SPLIT>((s0[2] + s1[2]) * c0, a.cap) - lse.x, x[3] = capped<SPLIT>((s0[3] + s1[3]) * c1, a.cap) - lse.y;
         } else {
           x[0] = fmaf(s0[0] + s1[0], c0, -lse.x), x[1] = fmaf(s0[1] + s1[1], c1, -lse.y);
           x[2] = fmaf(s0[2] + s1[2], c0, -lse.x), x[3] = fmaf(s0[3] + s1[3], c1, -lse.y);

@@ -355,11 +355,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
       auto qk = [&](int qt, int st) {
         const uint64_t q = dq + (uint32_t)(qt * (SPLIT ? 2 : 1) * L::kMat >> 4), k = dk + (uint32_t)(st * L::kStage >> 4);
 #pragma unroll
-        for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
+        for (int part = SPLIT ? 1 : 0; part >= 0; --part)  // (lo first: an accumulator cuts off what does not fit it)
 #pragma unroll
           for (int kk = 0; kk < HD / 16; ++kk) {
             const uint32_t off = (kk >> 2) * BLK + (kk & 3) * 32;
-            mma_ss(tmem + qt * 128, q + ((part * L::kMat + off) >> 4), k + (off >> 4), id_s, part > 0 || kk > 0, issue);
+            mma_ss(tmem + qt * 128, q + ((part * L::kMat + off) >> 4), k + (off >> 4), id_s, part < (SPLIT ? 1 : 0) || kk > 0,
+                   issue);
           }
         commit(&s_full[qt], issue);
       };
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const float y = x[i] * (coef * hd.ks[2 * c + (i >> 4)]);
-          x[i] = (b >> i) & 1u ? (cap ? capped(y, a.cap) : y) : -INFINITY;
+          x[i] = (b >> i) & 1u ? (cap ? capped<SPLIT>(y, a.cap) : y) : -INFINITY;
         }
       };
       // A plain tile's columns are asked for a chunk ahead; the others' loops stay rolled, so that the code fits the
