@@ -396,62 +396,100 @@ __global__ void __launch_bounds__(kSelThreads) k_kv8_select(Kv8SelectArgs a) {
   }
 }
 
-// Grid (blocks of the kept slots, heads).  A thread keeps its two chunks as codes, not values, over the reduction: a
-// row's index, page and codes are three round trips to memory, and what bounds the kernel is how many are under way.
+// The largest magnitude of sixteen codes under scale s, which is one product, since rounding keeps the codes' order.
+// NaN or infinite where a value is.
+template <int CODE>
+__device__ __forceinline__ float codes_amax(const uint4& u, float s) {
+  uint32_t h[8];
+  codes_to_half<CODE>(u.x, h[0], h[1]);
+  codes_to_half<CODE>(u.y, h[2], h[3]);
+  codes_to_half<CODE>(u.z, h[4], h[5]);
+  codes_to_half<CODE>(u.w, h[6], h[7]);
+  __half2 m = __habs2(*reinterpret_cast<const __half2*>(&h[0]));
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __half2*>(&h[i])));
+  return __fmul_rn(__half2float(__hmax_nan(__low2half(m), __high2half(m))), fabsf(s));
+}
+
+// Grid (CTAs, heads): a CTA takes every gridDim.x-th block of the kept slots.  A row's index, page and codes are three
+// round trips to memory, so they are asked for three, two and one blocks ahead.
 template <int FROM, int TO>
-__global__ void __launch_bounds__(kQuantThreads, 3) k_kv8_gather(Kv8View src, Kv8View dst, const int* index, int keep) {
-  __shared__ uint32_t red[3][32];
+__global__ void __launch_bounds__(kQuantThreads, 2) k_kv8_gather(Kv8View src, Kv8View dst, const int* index, int keep) {
+  __shared__ uint32_t red[2][3][32];
   const int h = blockIdx.y;
   const int rshift = dst.hd == 128 ? 3 : 2;
-  const int slot0 = blockIdx.x << dst.tshift;
+  const int t = threadIdx.x >> rshift, step = gridDim.x << dst.tshift;
+  const int chunk = (threadIdx.x - (t << rshift)) * 16;
+  struct Codes {
+    uint4 u[2];
+    float s[2];
+  };
   griddep_launch();
   griddep_wait();
-  const int page = dst.btab[slot0 / kPage];
-  const int t = threadIdx.x >> rshift;
-  const bool used = slot0 + t < keep;
-  uint4 u[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  float from[2] = {0.f, 0.f}, amax[2] = {0.f, 0.f}, odd = 0.f;
-  if (used) {
-    const int slot = __ldg(index + (size_t)h * keep + slot0 + t);
-    const int p = __ldg(src.btab + slot / kPage), in_page = slot % kPage;
-    if (src.page_ok(p)) {
-      const size_t at = src.page_row(p, h) + (size_t)in_page * src.hd + (threadIdx.x - (t << rshift)) * 16;
-      const size_t sc = src.scale_at(p, h, in_page);
-      u[0] = __ldg(reinterpret_cast<const uint4*>(src.k + at));
-      u[1] = __ldg(reinterpret_cast<const uint4*>(src.v + at));
-      from[0] = __ldg(src.ks + sc);
-      from[1] = __ldg(src.vs + sc);
+  index += (size_t)h * keep;
+  auto index_of = [&](int slot0) { return slot0 + t < keep ? __ldg(index + slot0 + t) : -1; };
+  auto page_of = [&](int slot) { return slot >= 0 ? __ldg(src.btab + slot / kPage) : -1; };
+  auto codes_of = [&](int slot, int page) {
+    Codes c = {{make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)}, {0.f, 0.f}};
+    if (src.page_ok(page)) {  // (a slot that is not one has page -1)
+      const size_t at = src.page_row(page, h) + (size_t)(slot % kPage) * src.hd + chunk;
+      const size_t sc = src.scale_at(page, h, slot % kPage);
+      c.u[0] = __ldg(reinterpret_cast<const uint4*>(src.k + at));
+      c.u[1] = __ldg(reinterpret_cast<const uint4*>(src.v + at));
+      c.s[0] = __ldg(src.ks + sc);
+      c.s[1] = __ldg(src.vs + sc);
     }
+    return c;
+  };
+  auto target = [&](int slot0) { return slot0 < keep ? dst.btab[slot0 / kPage] : -1; };
+  const int first = blockIdx.x << dst.tshift;
+  const int slot = index_of(first);
+  int to = target(first);
+  Codes now = codes_of(slot, page_of(slot));
+  int s2 = index_of(first + step), s3 = index_of(first + 2 * step), p2 = page_of(s2);
+  int round = 0;
+  for (int slot0 = first; slot0 < keep; slot0 += step, round ^= 1) {
+    const Codes next = codes_of(s2, p2);
+    s2 = s3;
+    p2 = page_of(s2);
+    s3 = index_of(slot0 + 3 * step);
+    const int page = to;
+    to = target(slot0 + step);
+    const bool used = slot0 + t < keep;
+    float amax[2], odd = 0.f;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      float x[16];
-      decode16<FROM>(u[w], from[w], x);
-      amax16(x, amax[w], odd);
+      amax[w] = codes_amax<FROM>(now.u[w], now.s[w]);
+      if (!(amax[w] < INFINITY)) amax[w] = 0.f, odd = NAN;
     }
-  }
-  if (!dst.page_ok(page)) return;
-  const bool any_odd = block_max2(amax[0], amax[1], odd, red);
-  if (any_odd) {
-    __syncthreads();
+    const bool any_odd = block_max2(amax[0], amax[1], odd, red[round]);
+    if (any_odd) {
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      float x[16];
-      decode16<FROM>(u[w], from[w], x);
-      amax[w] = used ? finite_amax16(x, 0.f) : 0.f;
+      for (int w = 0; w < 2; ++w) {
+        float x[16];
+        decode16<FROM>(now.u[w], now.s[w], x);
+        amax[w] = used ? finite_amax16(x, 0.f) : 0.f;
+      }
+      block_max2(amax[0], amax[1], 0.f, red[round]);
     }
-    block_max2(amax[0], amax[1], 0.f, red);
-  }
-  const size_t at = dst.page_row(page, h) + (size_t)(slot0 % kPage) * dst.hd + threadIdx.x * 16;
-  const size_t sc = dst.scale_at(page, h, slot0 % kPage);
+    if (dst.page_ok(page)) {
+      const size_t at = dst.page_row(page, h) + (size_t)(slot0 % kPage) * dst.hd + threadIdx.x * 16;
+      const size_t sc = dst.scale_at(page, h, slot0 % kPage);
+      // (the even lanes find K's scale, the odd ones V's)
+      const float mine = block_scale<TO>(threadIdx.x & 1 ? amax[1] : amax[0]), inv = inverse_scale(mine);
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const float s = block_scale<TO>(amax[w]);
-    if (used) {
-      float x[16];
-      decode16<FROM>(u[w], from[w], x);
-      store_codes<TO>((w ? dst.v : dst.k) + at, x, inverse_scale(s), any_odd);
+      for (int w = 0; w < 2; ++w) {
+        const float m = __shfl_sync(0xffffffffu, inv, w);
+        if (used) {
+          float x[16];
+          decode16<FROM>(now.u[w], now.s[w], x);
+          store_codes<TO>((w ? dst.v : dst.k) + at, x, m, any_odd);
+        }
+      }
+      if (threadIdx.x < 2) (threadIdx.x ? dst.vs : dst.ks)[sc] = mine;
     }
-    if (threadIdx.x == 0) (w ? dst.vs : dst.ks)[sc] = s;
+    now = next;
   }
 }
 
@@ -496,8 +534,10 @@ bool launch_kv8_evict(const Kv8View& src, const Kv8View& dst, const Kv8SelectArg
   const auto gather = src.code == KV8_INT8
                           ? (dst.code == KV8_INT8 ? k_kv8_gather<KV8_INT8, KV8_INT8> : k_kv8_gather<KV8_INT8, KV8_E4M3>)
                           : (dst.code == KV8_INT8 ? k_kv8_gather<KV8_E4M3, KV8_INT8> : k_kv8_gather<KV8_E4M3, KV8_E4M3>);
-  return launch_kv8(gather, dim3(((a.keep - 1) >> dst.tshift) + 1, src.n_kv), (dst.hd / 16) << dst.tshift, 0, st, 1, src, dst,
-                    (const int*)a.index, a.keep);
+  const int threads = (dst.hd / 16) << dst.tshift, blocks = ((a.keep - 1) >> dst.tshift) + 1;
+  const int fit = (152 * 2 * kQuantThreads / threads + src.n_kv - 1) / src.n_kv;  // CTAs of a head that run at once
+  const int per = (blocks + fit - 1) / fit;
+  return launch_kv8(gather, dim3((blocks + per - 1) / per, src.n_kv), threads, 0, st, 1, src, dst, (const int*)a.index, a.keep);
 }
 
 }  // namespace ssd
