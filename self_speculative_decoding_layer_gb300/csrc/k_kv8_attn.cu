@@ -10,16 +10,31 @@
 // queries of one KV head the N dimension, so the group of a decoded token
 // fills the tile.  Codes are exact in fp16; a query row is scaled by a power
 // of two and, when it is fp32, split into hi + lo (22 bits), and so are its
-// softmax weights.  Every warp takes sixteen-key tiles of its own, straight
-// from global memory into registers (a lane's sixteen bytes of a row are the
-// MMA's k indices in an order that Q is laid out to match), and keeps a
-// running maximum, sum and O^T in registers; warps and CTAs merge at the end
-// in a fixed order.  A tile lies inside one scale block, so its scales are
-// one number each.
+// softmax weights (16-bit queries keep 11 bits of a weight, less than their
+// output's own rounding).  Every warp takes 32-slot tiles of its own: codes by
+// cp.async into its ring in shared memory, from there into registers (a lane's
+// sixteen bytes of a row are the MMA's k indices in an order that Q is laid
+// out to match), and keeps a running maximum, sum and O^T in registers; warps
+// and CTAs merge at the end in a fixed order.  A tile's halves of sixteen
+// slots lie inside one scale block each, so a half's scales are one number.
+//
+// What bounds it (one GB300, times of a captured call):
+//   one bf16 token, 64 heads on 8, 65532 e4m3 slots (134 MB): 26.8 us, 5.0 TB/s
+//     of a copy's 6.8; 23 us of it are the stream, at 63 % of the DRAM's cycles
+//     with a third of the ALU's for the conversions, the rest the merge kernel;
+//   7 fp32 rows, 32 heads on 8, 4100 int8 slots: 14.2 us, a tile for every
+//     warp: latency (staging, one tile, two merges); MMAs are 17 % of it;
+//   one fp32 token, 32 heads on 8, 641 slots: 7.2 us, latency.
+// Chunks of many queries run on the fifth-generation tensor cores instead
+// (launch_kv8_attention_tc).
 //
 // k_kv8_weights recomputes the scores and adds exp(s - lse) over the chosen
 // rows and the KV head's queries to an accumulator: each sixteen-slot tile is
-// one warp's, so nothing is shared and the sums have one order.
+// one warp's, so nothing is shared and the sums have one order.  5 rows of 64
+// heads on 8 over 32776 e4m3 slots: 16.0 us, 36 MB (2.2 TB/s); bound by the
+// MMAs and exponentials of 40 queries a slot, 28 and 24 % of their pipes, and
+// the latency between them (three CTAs an SM: 18.9 us; K two tiles ahead:
+// 18.0).
 #include <cooperative_groups.h>
 
 #include "kv8_attn.cuh"
@@ -549,7 +564,9 @@ __global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(
   }
 }
 
-// Grid (queries of all heads): thread t adds dim t of its query over the splits, in order.
+// Grid (queries of all heads): thread t adds dim t of its query over the splits, in order.  About 3 us behind the kernel
+// before it, most of that one launch and two round trips to L2.  (A warp for each query: 1.0 to 1.8 us longer for one
+// token to 28 queries a head, 0.9 shorter for 512.)
 template <typename T, int HD>
 __global__ void __launch_bounds__(HD) k_kv8_merge(const __grid_constant__ Kv8AttnArgs a) {
   __shared__ float2 s_f[kMaxSplits];

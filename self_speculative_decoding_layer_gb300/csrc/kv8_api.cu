@@ -1,5 +1,5 @@
 // The 8-bit KV cache's entry points: argument checks, then the kernels of
-// k_kv8.cu and k_kv8_attn.cu on the caller's stream.
+// k_kv8.cu, k_kv8_attn.cu and k_kv8_attn_tc.cu on the caller's stream.
 #include <math.h>
 
 #include "../../include/ssd.h"

@@ -1,8 +1,8 @@
 // Python binding of the 8-bit KV cache (ssd_kv8_* of include/ssd.h) for torch
 // tensors: argument checks, output and scratch allocation, the current stream.
-// A decoded token's kernels run for a few microseconds, and the same checks
-// and marshalling in Python with ctypes took 14 to 21 us a call; kv8.py is a
-// thin layer over this module.
+// A decoded token's kernels run for 3 to 7 us.  The same checks and
+// marshalling in Python with ctypes took 14 to 21 us a call, and 2 to 5
+// here; kv8.py is a thin layer over this module.
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
