@@ -34,7 +34,8 @@ namespace {
 constexpr int kTcTile = 128;      // slots of a tile
 constexpr int kConvWarps = 8;
 constexpr int kMmaWarp = 8 + kConvWarps;
-constexpr int kTcThreads = (kMmaWarp + 1) * 32;  // warps 0-3 and 4-7: softmax of query blocks 0 and 1; converters; MMA
+constexpr int kTcThreads = (kMmaWarp + 2) * 32;  // warps 0-3 and 4-7: softmax of query blocks 0 and 1; converters; the
+                                                 // blocks' MMA issuers (one for both waits for the block whose turn it is)
 constexpr int kTcStages = 2;
 constexpr float kTcShift = 9.f;   // softmax weights are held times 2^9, and grow to 2^(9 + kSlack) < 2^16
 constexpr float kSlack = 6.f;
@@ -164,13 +165,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
   uint64_t* kv_empty = bars + kTcStages;      // [stages] MMA -> converters
   uint64_t* s_full = kv_empty + kTcStages;    // [NQT] MMA -> softmax
   uint64_t* p_full = s_full + NQT;            // [NQT] softmax -> MMA
-  uint64_t* pv_done = p_full + NQT;           // [NQT] MMA -> softmax
+  uint64_t* pv_done = p_full + NQT;           // [NQT] MMA -> softmax, after the last tile
   __shared__ uint32_t s_tmem;
   __shared__ float s_red[kConvWarps], s_vref;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x, h = blockIdx.y, q0 = blockIdx.z * 128 * NQT;
   const int nq = a.rows * a.group;
-  const int n_act = min(NQT, (nq - q0 + 127) / 128);  // query blocks in use
+  const int n_act = min(NQT, (nq - q0 + 127) / 128);  // query blocks in use, one at least
   griddep_launch();
   const Tiles<7> tiles(a.prefix, a.base, a.rows);
   const int t_first = min(tiles.n, split * a.split_tiles), t_last = min(tiles.n, t_first + a.split_tiles);
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
     if (lane == 0) {
       for (int i = 0; i < kTcStages; ++i) {
         mbar_init(&kv_full[i], kConvWarps * 32);
-        mbar_init(&kv_empty[i], 1);
+        mbar_init(&kv_empty[i], n_act);
       }
       for (int i = 0; i < NQT; ++i) {
         mbar_init(&s_full[i], 1);
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
   }
   // Queries: a warp takes eight at a time (all of their loads first), as fp16 rows times their power of two.
   constexpr int QG = 8;
-  for (int g0 = (warp < 8 ? warp : 8) * QG; !converter && g0 < n_act * 128; g0 += 9 * QG) {
+  for (int g0 = (warp < 8 ? warp : warp - kConvWarps) * QG; !converter && g0 < n_act * 128; g0 += 10 * QG) {
     float2 x[QG][HB];
     int r = (q0 + g0) / a.group, e = q0 + g0 - r * a.group;
 #pragma unroll
@@ -351,15 +352,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
       p0 = n0;
       p1 = n1;
     }
-  } else if (warp == kMmaWarp) {
-    if (n_tile > 0) {
+  } else if (warp >= kMmaWarp) {
+    const int qt = warp - kMmaWarp;
+    if (n_tile > 0 && qt < n_act) {
       // ---- MMA issuer
       const uint32_t issue = lane == 0;
       constexpr uint32_t id_s = idesc_h(kTcTile, false), id_o = idesc_h(HD, true);
       const uint64_t dq = desc_k(smem_u32(s_q)), dk = desc_k(smem_u32(s_kv));
       const uint64_t dv = desc_mn(smem_u32(s_kv) + L::kMat, BLK);
       // (descriptors count addresses in sixteen bytes; all of shared memory fits their field)
-      auto qk = [&](int qt, int st) {
+      auto qk = [&](int st) {
         const uint64_t q = dq + (uint32_t)(qt * (SPLIT ? 2 : 1) * L::kMat >> 4), k = dk + (uint32_t)(st * L::kStage >> 4);
 #pragma unroll
         for (int part = SPLIT ? 1 : 0; part >= 0; --part)  // (lo first: an accumulator cuts off what does not fit it)
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
           }
         commit(&s_full[qt], issue);
       };
-      auto pv = [&](int qt, int st, bool first) {
+      auto pv = [&](int st, bool first) {
         const uint64_t v = dv + (uint32_t)(st * L::kStage >> 4);
 #pragma unroll
         for (int part = 0; part < (SPLIT ? 2 : 1); ++part)
@@ -379,26 +381,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
           for (int kk = 0; kk < kTcTile / 16; ++kk)
             mma_ts(tmem + c_o + qt * 128, tmem + (part ? c_lo : qt * 128) + kk * 8, v + kk * (2048 >> 4), id_o,
                    !(first && part == 0 && kk == 0), issue);
-        commit(&pv_done[qt], issue);
       };
       bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&kv_full[0], 0u));
       fence_after();
-      for (int qt = 0; ok && qt < n_act; ++qt) qk(qt, 0);
+      if (ok) qk(0);
       for (int j = 0; ok && j < n_tile; ++j) {
-        for (int qt = 0; qt < n_act; ++qt) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&p_full[qt], (uint32_t)j & 1u));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&p_full[qt], (uint32_t)j & 1u));
+        if (!ok) break;
+        fence_after();
+        pv(j & 1, j == 0);
+        commit(&kv_empty[j & 1], issue);
+        if (j + 1 < n_tile) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&kv_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u));
           if (!ok) break;
           fence_after();
-          pv(qt, j & 1, j == 0);
-          if (qt == n_act - 1) commit(&kv_empty[j & 1], issue);
-          if (j + 1 < n_tile) {
-            if (qt == 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait_bounded(&kv_full[(j + 1) & 1], (uint32_t)((j + 1) >> 1) & 1u));
-              if (!ok) break;
-              fence_after();
-            }
-            qk(qt, (j + 1) & 1);
-          }
+          qk((j + 1) & 1);
+        } else {
+          commit(&pv_done[qt], issue);
         }
       }
     }
@@ -464,10 +463,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
         const float f = lags ? exp2_approx(m - top) : 1.f;  // (m = -inf: 0)
         if (lags) m = top;
         l *= f;
-        if (j > 0) {
-          ok = mbar_wait_bounded(&pv_done[qt], (uint32_t)(j - 1) & 1u);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          fence_after();
+        if (j > 0) {  // (the products of the tiles before are in O: they were committed before these scores)
 #pragma unroll 1
           for (int c = 0; c < HD / 32; ++c) {
             float x[32];
@@ -528,7 +524,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
       arrive(&p_full[qt]);
     }
     // ---- output
-    if (n_tile > 0 && __all_sync(0xffffffffu, ok)) ok = mbar_wait_bounded(&pv_done[qt], (uint32_t)(n_tile - 1) & 1u);
+    if (n_tile > 0 && __all_sync(0xffffffffu, ok)) ok = mbar_wait_bounded(&pv_done[qt], 0u);
     if (__all_sync(0xffffffffu, ok)) {
       fence_after();
       const float vref = n_tile > 0 ? *(volatile float*)&s_vref : 0.f;
@@ -536,6 +532,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
       const size_t at = ((size_t)h * nq + qi) * a.n_split + split;
       const float f = a.part_o ? vref : l == 0.f ? 0.f : vref / l;
       const float top = m + (kPShift - kTcShift);
+      float4* s_rows = reinterpret_cast<float4*>(s_q + qt * (SPLIT ? 2 : 1) * L::kMat + (warp & 3) * 4096);
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
         float x[32];
@@ -545,14 +542,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = 0.f;
         }
-        if (qi < nq) {
+        // Rows to coalesced lines, through the block's queries, which no MMA reads any more: 32 rows of 32 columns a
+        // warp, chunks swizzled by the row.  (A row for each thread, as TMEM has them: 8 us for 512 queries a head.)
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float4 y = make_float4(x[i] * f, x[i + 1] * f, x[i + 2] * f, x[i + 3] * f);
-            if (a.part_o)
-              *reinterpret_cast<float4*>(a.part_o + at * HD + c * 32 + i) = y;
-            else
-              store4(reinterpret_cast<T*>(a.out) + (size_t)r * a.ld_out + (size_t)head * HD + c * 32 + i, y);
+        for (int i = 0; i < 8; ++i)
+          s_rows[lane * 8 + (i ^ (lane & 7))] = make_float4(x[4 * i] * f, x[4 * i + 1] * f, x[4 * i + 2] * f, x[4 * i + 3] * f);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = i * 4 + (lane >> 3), to_q = qi - lane + row;
+          const float4 y = s_rows[row * 8 + ((lane & 7) ^ (row & 7))];
+          if (to_q >= nq) continue;
+          const int col = c * 32 + (lane & 7) * 4;
+          if (a.part_o) {
+            *reinterpret_cast<float4*>(a.part_o + (((size_t)h * nq + to_q) * a.n_split + split) * HD + col) = y;
+          } else {
+            const int to_r = to_q / a.group;
+            store4(reinterpret_cast<T*>(a.out) + (size_t)to_r * a.ld_out + (size_t)(h * a.group + to_q - to_r * a.group) * HD + col,
+                   y);
           }
         }
       }
