@@ -5,16 +5,20 @@
 // 128-slot tiles.  S = Q K^T and O += P V run as 128-wide fp16 tcgen05.mma
 // with fp32 accumulators in TMEM: Q, K and V come from shared memory (128-byte
 // swizzle; V as stored, key by key, is the transposed operand), P from TMEM,
-// where the softmax writes it over S.  What one tensor-core pass cannot do is
-// what bounds it: every code becomes fp16 once for all of the CTA's queries
-// (eight converter warps, which also prefetch the next tile's codes in
-// registers), and every score is read twice from TMEM by its row's thread
-// (once for the maximum, once for the exponential).  64 bf16 rows of 64 heads
-// on 8 over 16448 int8 slots, 34.4 GFLOP: 60 us, 0.57 PFLOP/s, the tensor
-// pipe busy for 27 % and the ALU for 26: the softmax's chain from TMEM through
-// the maximum, the exponentials and back is longer than the MMAs of the other
-// block that it runs beside.  (One pass over the scores, the maximum checked
-// chunk by chunk, spilled: 70 to 77 us.)
+// where the softmax writes it over S.  Every code becomes fp16 once for all of
+// the CTA's queries (eight converter warps, which also prefetch the next
+// tile's codes in registers), and every score is read twice from TMEM by its
+// row's thread (once for the maximum, once for the exponential).
+//
+// 64 bf16 rows of 64 heads on 8 over 16448 int8 slots, 34.4 GFLOP: 57 us with
+// the merge, 0.6 PFLOP/s, the tensor pipe busy for 27 % and the ALU for 26.
+// What bounds it is latency: of about 4800 clocks a tile each block spends
+// 1900 to 2700 in its softmax (1000 of them the exponentials of two warps a
+// scheduler) and the rest between its weights and its next scores, where the
+// MMAs take 75 to 150 clocks instead of 64 beside the other block's softmax.
+// Measured worse: one pass over the scores with the maximum checked chunk by
+// chunk (it spilled, 70 to 77 us), one issuer for both blocks (60.4), stages
+// of K and V released apart (59.2), softmaxes that take turns (70).
 //
 // fp32 queries are split into hi + lo, and so are their softmax weights; they
 // run one block of 128 queries, 16-bit ones two, whose softmax and MMAs
@@ -166,6 +170,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
   uint64_t* s_full = kv_empty + kTcStages;    // [NQT] MMA -> softmax
   uint64_t* p_full = s_full + NQT;            // [NQT] softmax -> MMA
   uint64_t* pv_done = p_full + NQT;           // [NQT] MMA -> softmax, after the last tile
+  uint64_t* turn = pv_done + NQT;             // issuer of block 0 -> of block 1
   __shared__ uint32_t s_tmem;
   __shared__ float s_red[kConvWarps], s_vref;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -191,6 +196,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
         mbar_init(&p_full[i], 128);
         mbar_init(&pv_done[i], 1);
       }
+      mbar_init(turn, 1);
       fence_barrier_init();
     }
   }
@@ -231,6 +237,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
     const size_t a0 = page_at(p0), a1 = page_at(p1);
 #pragma unroll
     for (int i = 0; i < NI; ++i) load(i, 0, RS * i < kPage ? p0 : p1, RS * i < kPage ? a0 : a1, whole_of(0));
+  }
+  float vref = 1.f;
+  if (converter) {  // (while the other warps stage the queries)
+    float vmax = 0.f;  // V's largest scale in the split
+    for (int i = ct; i < n_tile * 8; i += kConvWarps * 32) {
+      const int slot = tiles.slot(t_first + (i >> 3)) + (i & 7) * 16;
+      if (!visible_any(slot, a)) continue;
+      const int page = __ldg(a.c.btab + slot / kPage);
+      if (a.c.page_ok(page)) vmax = fmaxf(vmax, __ldg(a.c.vs + a.c.scale_at(page, h, slot % kPage)));
+    }
+    vmax = warp_max(vmax);
+    if (lane == 0) s_red[warp - 8] = vmax;
+    asm volatile("bar.sync 1, %0;" ::"n"(kConvWarps * 32) : "memory");
+    vmax = warp_max(s_red[lane % kConvWarps]);
+    vref = vmax > 0.f ? vmax : 1.f;
+    if (ct == 0) s_vref = vref;
   }
   // Queries: a warp takes eight at a time (all of their loads first), as fp16 rows times their power of two.
   constexpr int QG = 8;
@@ -274,20 +296,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
 
   if (converter) {
     // ---- converters
-    float vmax = 0.f;  // V's largest scale in the split
-    for (int i = ct; i < n_tile * 8; i += kConvWarps * 32) {
-      const int slot = tiles.slot(t_first + (i >> 3)) + (i & 7) * 16;
-      if (!visible_any(slot, a)) continue;
-      const int page = __ldg(a.c.btab + slot / kPage);
-      if (a.c.page_ok(page)) vmax = fmaxf(vmax, __ldg(a.c.vs + a.c.scale_at(page, h, slot % kPage)));
-    }
-    vmax = warp_max(vmax);
-    if (lane == 0) s_red[warp - 8] = vmax;
-    asm volatile("bar.sync 1, %0;" ::"n"(kConvWarps * 32) : "memory");
-    vmax = warp_max(s_red[lane % kConvWarps]);
-    const float vref = vmax > 0.f ? vmax : 1.f;
-    if (ct == 0) s_vref = vref;
-
     int t0 = page_of(1, 0), t1 = page_of(1, 1);
     for (int j = 0; j < n_tile; ++j) {
       const int st = j & 1, n0 = checked(t0), n1 = checked(t1);
@@ -383,11 +391,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
                    !(first && part == 0 && kk == 0), issue);
       };
       bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&kv_full[0], 0u));
+      // (block 1 starts when block 0 has its first weights, so that their softmaxes do not begin side by side)
+      if (NQT == 2 && qt == 1 && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(turn, 0u));
       fence_after();
       if (ok) qk(0);
       for (int j = 0; ok && j < n_tile; ++j) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&p_full[qt], (uint32_t)j & 1u));
         if (!ok) break;
+        if (NQT == 2 && qt == 0 && j == 0 && lane == 0) arrive(turn);
         fence_after();
         pv(j & 1, j == 0);
         commit(&kv_empty[j & 1], issue);
