@@ -830,15 +830,18 @@ bool weights_of(const Kv8AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// The tcgen05 kernel runs where a KV head has more than 32 queries and the 32-query blocks times the slots of all heads
-// reach this many (64 rows of 64 query heads on 8, bf16: over 1500 slots, 192000 of these units, it takes 31.0 us and the
-// other 26.7; over 4000 33.3 and 49.3; over 16000 61.0 and 156.  64 queries a head: over 16000, 256000 units, 29.5 and
-// 30.2.  64 rows of 40 heads: over 1500, 120000 units, 26.5 and 26.7, over 4000 35.8 and 51.1).
-constexpr long long kTcWork = 200000;
+// The tcgen05 kernel runs where a KV head has more than 64 queries and the 32-query blocks times the slots of all heads
+// reach kTcWork (us, this kernel and the other, on heads 64 over 8: 64 bf16 rows over 1564 slots, 200192 of these units,
+// 27.5 and 26.2; 24 rows over 4024, 193152, 23.8 and 24.8; 64 rows over 16064 59.9 and 159; fp32 24 rows over 4024 36.8
+// and 31.8, 64 over 4064 51.0 and 67.9).  Of 33 to 64 queries, which fill half a block at most, only 16-bit ones, and
+// from kTcWorkHalf on (5 bf16 rows over 16005 slots, 256080 units, 30.8 and 28.9, and 0.95 and 1.1 us for every thousand
+// slots more; fp32 48.3 and 37.0, 1.4 and 1.6).
+constexpr long long kTcWork = 200000, kTcWorkHalf = 500000;
 
 Kv8Splits kv8_attention_splits(int rows, int group, int n_kv, int slots, int io) {
   const int nq = rows * group;
-  const bool tc = nq > 32 && (long long)n_kv * ((nq + 31) / 32) * slots >= kTcWork;
+  const long long work = (long long)n_kv * ((nq + 31) / 32) * slots;
+  const bool tc = nq > 64 ? work >= kTcWork : nq > 32 && io != 2 && work >= kTcWorkHalf;
   const int qb = tc ? (io == 2 ? 128 : 256) : 8 * query_eights(nq);
   const int blocks = n_kv * ((nq + qb - 1) / qb);
   const int slots_a_tile = tc ? 128 : kTileSlots;

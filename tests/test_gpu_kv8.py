@@ -174,6 +174,9 @@ ATTN = [  # rows, prefix, base - prefix, masks, hq, hkv, hd, code, block, io, ca
     (64, 4300, -20, "tree", 24, 3, 128, "e4m3", 64, "fp16", 0.0),
     (40, 100013, 0, "own", 1, 1, 64, "int8", 32, "bf16", 0.0),
     (64, 0, 3300, "holes", 40, 40, 64, "int8", 64, "fp32", 0.0),
+    (17, 9000, 0, "tree", 40, 5, 128, "e4m3", 32, "fp32", 0.0),
+    (17, 9000, 3, "causal", 40, 5, 128, "int8", 16, "fp32", 20.0),
+    (40, 6300, 0, "tree", 40, 40, 64, "e4m3", 32, "bf16", 0.0),  # and with half a block
     (3, 0, 0, "holes", 6, 3, 64, "e4m3", 16, "fp32", 0.0),  # a row that sees nothing
     (9, 77, 40, "none", 10, 10, 128, "int8", 16, "fp16", 0.0),
     (6, 100, -10, "tree", 21, 3, 64, "int8", 32, "fp32", 50.0),  # new slots that the prefix holds already count once
