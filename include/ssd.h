@@ -544,6 +544,7 @@ ssd_status ssd_kv8_read(const ssd_kv8_cache* cache, const ssd_kv8_rows* rows, vo
  *        ld_lse and step_lse elements between rows and between heads (both 0: n_q_heads and 1)
  *   dtype of q and out: SSD_F32, SSD_BF16 or SSD_FP16; 16-byte aligned, rows a multiple of 16 bytes apart
  *   scores are scale * q.k (scale > 0), with softcap > 0 then softcap * tanh(score / softcap)
+ *        (softcap 0: none, else 1e-30 to 1e30; with a 16-bit q its rounding may move a score by softcap * 2^-22)
  * Sums and softmax statistics are fp32; an fp32 q is not rounded below 22
  * bits.  A row that sees no slot gets zeros and lse -inf; slots that a row
  * does not see may hold anything, those past every row's sight need never

@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(
   __syncthreads();
 
   const bool cap = a.cap > 0.f;
+  const float inv_cap = cap ? 1.f / a.cap : 0.f;
   float coef[QT][2];
   float m[QT][2], l[QT][2], o[QT][DT][4];
   float vref = 0.f, vinv = 0.f;  // O^T is held in units of vref, a scale of V
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(AttnShape<HD, QT>::W * 32, 1) k_kv8_attention(
 #pragma unroll
         for (int t = 0; t < QT; ++t)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[b][t][e] = capped<SPLIT>(s[b][t][e], a.cap);
+          for (int e = 0; e < 4; ++e) s[b][t][e] = capped<SPLIT>(s[b][t][e], a.cap, inv_cap);
     }
     if (!full) {
       vmax = fmaxf(visible_any(slot0, a) ? head.vs[0] : 0.f, visible_any(slot0 + 16, a) ? head.vs[1] : 0.f);
@@ -641,6 +642,7 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
   const int n_tiles = (n_slots + 15) >> 4, stride = gridDim.x * kWWarps;
   const int first = blockIdx.x * kWWarps + warp;
   const int nq = a.n_take * a.group;
+  const float inv_cap = CAP ? 1.f / a.cap : 0.f;
   griddep_launch();
   griddep_wait();
 
@@ -734,8 +736,9 @@ __global__ void __launch_bounds__(kWWarps * 32, 2) k_kv8_weights(const __grid_co
         const float2 lse = *reinterpret_cast<const float2*>(s_lse + t * 8 + 2 * c);
         const float c0 = cf.x * ks, c1 = cf.y * ks;
         if (CAP) {
-          x[0] = capped<SPLIT>((s0[0] + s1[0]) * c0, a.cap) - lse.x, x[1] = capped<SPLIT>((s0[1] + s1[1]) * c1, a.cap) - lse.y;
-          x[2] = capped<SPLIT>((s0[2] + s1[2]) * c0, a.cap) - lse.x, x[3] = capped<SPLIT>((s0[3] + s1[3]) * c1, a.cap) - lse.y;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = capped<SPLIT>((s0[e] + s1[e]) * (e & 1 ? c1 : c0), a.cap, inv_cap) - (e & 1 ? lse.y : lse.x);
         } else {
           x[0] = fmaf(s0[0] + s1[0], c0, -lse.x), x[1] = fmaf(s0[1] + s1[1], c1, -lse.y);
           x[2] = fmaf(s0[2] + s1[2], c0, -lse.x), x[3] = fmaf(s0[3] + s1[3], c1, -lse.y);

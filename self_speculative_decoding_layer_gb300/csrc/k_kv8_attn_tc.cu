@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + qt * 128, tl = tmem + lanes + c_lo, to = tmem + lanes + c_o + qt * 128;
     const bool cap = a.cap > 0.f;
+    const float inv_cap = cap ? 1.f / a.cap : 0.f;
     const float coef = a.scale * s_inv[qt * 128 + row] * (cap ? 1.f : kLog2e);
     const unsigned long long mask = qi < nq ? a.mask[qi / a.group] : 0ull;
     float m = -INFINITY, l = 0.f;
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after();
       const TcHead& hd = s_head[st];
-      const bool full = hd.full && !cap;
+      const bool full = hd.full;
       const int slot0 = tiles.slot(t_first + j);
       // scores of 32 columns in the log2 domain, where the tile is not plain
       auto slow = [&](float (&x)[32], int c) {
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const float y = x[i] * (coef * hd.ks[2 * c + (i >> 4)]);
-          x[i] = (b >> i) & 1u ? (cap ? capped<SPLIT>(y, a.cap) : y) : -INFINITY;
+          x[i] = (b >> i) & 1u ? (cap ? capped<SPLIT>(y, a.cap, inv_cap) : y) : -INFINITY;
         }
       };
       // A plain tile's columns are asked for a chunk ahead; the others' loops stay rolled, so that the code fits the
@@ -459,6 +460,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
           if (c < 3) tmem_ld32_async(ts + (c + 1) * 32, x[(c + 1) & 1]);
           top = fmaxf(top, fmaxf(max16(x[c & 1]) * (coef * hd.ks[2 * c]), max16(x[c & 1] + 16) * (coef * hd.ks[2 * c + 1])));
         }
+        if (cap) top = capped<SPLIT>(top, a.cap, inv_cap);  // (the cap keeps the order, to its rounding)
       } else {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
         tmem_st16(ts + c * 16, hi);
         if (SPLIT) tmem_st16(tl + c * 16, lo);
       };
-      if (full) {
+      if (full && !cap) {
         uint32_t x[2][32];
         tmem_ld32_async(ts, x[0]);
 #pragma unroll

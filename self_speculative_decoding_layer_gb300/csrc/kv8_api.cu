@@ -70,7 +70,7 @@ bool attn_args(const ssd_kv8_cache* c, const ssd_kv8_attention_args* p, Kv8AttnA
   if (!rows_ok(p->q, p->ld_q, (int64_t)p->n_q_heads * c->head_dim, p->dtype)) return false;
   if (p->lse && !aligned(p->lse, 4)) return false;
   if (!(p->scale > 0.f) || !isfinite(p->scale) || !(p->softcap >= 0.f) || !isfinite(p->softcap)) return false;
-  if (p->softcap > 0.f && p->softcap < 1e-30f) return false;  // (its inverse has to be a number)
+  if (p->softcap > 0.f && !(p->softcap >= 1e-30f && p->softcap <= 1e30f)) return false;  // (its inverse has to be a number)
   a->q = p->q;
   a->ld_q = (size_t)p->ld_q;
   a->lse = p->lse;

@@ -54,17 +54,17 @@ __device__ __forceinline__ bool visible_any(int slot, const Kv8AttnArgs& a) {
   return ((e >= 0 ? a.any >> e : a.any << -e) & 0xffffull) != 0;
 }
 
-// The capped score in the log2 domain.  For 16-bit queries tanh y = 1 - 2 / (1 + e^2y), whose error of a few 2^-24 is
+// The capped score in the log2 domain, inv = 1 / cap.  For 16-bit queries tanh y = 1 - 2 / (1 + e^2y), whose error of a few 2^-24 is
 // absolute, so that a score is off by that many parts of the cap.  EXACT (fp32 queries): below 0.7 Lambert's fraction
 // y / (1 + y^2 / (3 + y^2 / (5 + y^2 / (7 + y^2 / 9)))), off by less than y^10 / 9.8e6 of the value, and (e^2y - 1) /
 // (e^2y + 1) above, each a few 2^-24 of the value.
 template <bool EXACT>
-__device__ __forceinline__ float capped(float x, float cap) {
+__device__ __forceinline__ float capped(float x, float cap, float inv) {
   if (!EXACT) {
-    const float e = exp2_approx(x * (2.f * kLog2e / cap));
+    const float e = exp2_approx(x * (2.f * kLog2e * inv));
     return cap * kLog2e * (1.f - __fdividef(2.f, 1.f + e));
   }
-  const float y = x * (1.f / cap), z = y * y;
+  const float y = x * inv, z = y * y;
   const float e = exp2_approx((y > 10.f ? 10.f : y) * (2.f * kLog2e));
   const bool small = fabsf(y) < 0.7f;
   const float num = small ? y * fmaf(z, z + 105.f, 945.f) : e - 1.f;

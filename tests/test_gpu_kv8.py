@@ -669,3 +669,20 @@ def test_a_fresh_cache():
         assert torch.equal(k, x) and torch.equal(v, 2 * x)
         o = c.attention(1, x / 448, 0)
         assert torch.allclose(o, 2 * x, rtol=2.0 ** -20, atol=0)  # a mean of equal values
+
+
+@pytest.mark.parametrize("rows,prefix,hq,hkv", [(3, 300, 16, 4), (17, 9000, 40, 5)], ids=str)
+def test_a_cap_far_above_the_scores_of_fp32_queries(rows, prefix, hq, hkv):
+    """tanh y = y (1 - y^2 / 3 ..), so under a cap of 1e6 a score s moves by less than s^3 / 3e12, and by its roundings:
+    the product with 1 / cap, two sums of three products each, the quotient (two steps), the product with cap: ten of
+    2^-24 of it at most.  A weight moves by that times e^.., twice with its sum, and the output by that times the values."""
+    case = (rows, prefix, 0, "causal", hq, hkv, 128, "int8", 32, "fp32", 0.0)
+    p, q, m, _, n, base = attention_case(case)
+    plain = p.gpu.attention(1, q.cuda(), prefix, base, masks=m).double()
+    capped = p.gpu.attention(1, q.cuda(), prefix, base, masks=m, softcap=1e6).double()
+    k, v = (torch.tensor(t.values(np.arange(n))) for t in (p.k, p.v))
+    s = float(q.float().norm(dim=-1).max() * k.float().norm(dim=-1).max()) / math.sqrt(128)
+    move = s ** 3 / 3e12 + 10 * s * 2.0 ** -24 + 4 * s * 2.0 ** -24  # (and each call's own scores, rounded twice)
+    assert move < 0.01
+    limit = 2.1 * move + 2 * 2.0 ** -22  # (either call's exponentials and 22-bit weights)
+    assert float((plain - capped).abs().max()) <= limit * float(v.abs().max())

@@ -80,7 +80,7 @@ def test_bad_rows(lib, bad):
 BAD_ATTN = [dict(q=None), dict(q=A + 4), dict(ld_q=4095), dict(ld_q=4097), dict(dtype=3), dict(n_q_heads=12),
             dict(n_q_heads=0), dict(n_q_heads=8 * 4097, ld_q=8 * 4097 * 128), dict(ld_q=2 ** 62), dict(rows=0), dict(rows=65), dict(prefix=-1), dict(prefix=257), dict(base=-1), dict(base=256),
             dict(base=2 ** 31 - 1), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan),
-            dict(softcap=-1.0), dict(softcap=1e-35), dict(softcap=math.inf), dict(softcap=math.nan), dict(lse=A + 2), dict(ld_lse=-1),
+            dict(softcap=-1.0), dict(softcap=1e-35), dict(softcap=1e31), dict(softcap=math.inf), dict(softcap=math.nan), dict(lse=A + 2), dict(ld_lse=-1),
             dict(step_lse=-4), dict(ld_lse=2 ** 50)]
 
 
