@@ -442,11 +442,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_kv8_attention_tc(const __grid
       // scores of 32 columns in the log2 domain, where the tile is not plain
       auto slow = [&](float (&x)[32], int c) {
         const uint32_t b = bits_of(slot0 + c * 32, (hd.ok >> (c >> 1)) & 1);
+        const float f[2] = {coef * hd.ks[2 * c], coef * hd.ks[2 * c + 1]};
+        if (cap) {  // (apart from the masks, so that the elements' chains overlap)
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float y = x[i] * (coef * hd.ks[2 * c + (i >> 4)]);
-          x[i] = (b >> i) & 1u ? (cap ? capped<SPLIT>(y, a.cap, inv_cap) : y) : -INFINITY;
+          for (int i = 0; i < 32; ++i) x[i] = capped<SPLIT>(x[i] * f[i >> 4], a.cap, inv_cap);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] *= f[i >> 4];
         }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = (b >> i) & 1u ? x[i] : -INFINITY;
       };
       // A plain tile's columns are asked for a chunk ahead; the others' loops stay rolled, so that the code fits the
       // instruction cache.

@@ -66,10 +66,10 @@ __device__ __forceinline__ float capped(float x, float cap, float inv) {
   }
   const float y = x * inv, z = y * y;
   const float e = exp2_approx((y > 10.f ? 10.f : y) * (2.f * kLog2e));
+  const float n0 = y * fmaf(z, z + 105.f, 945.f), d0 = fmaf(z, fmaf(z, 15.f, 420.f), 945.f);
+  const float n1 = e - 1.f, d1 = e + 1.f;
   const bool small = fabsf(y) < 0.7f;
-  const float num = small ? y * fmaf(z, z + 105.f, 945.f) : e - 1.f;
-  const float den = small ? fmaf(z, fmaf(z, 15.f, 420.f), 945.f) : e + 1.f;
-  return cap * kLog2e * __fdividef(num, den);
+  return cap * kLog2e * __fdividef(small ? n0 : n1, small ? d0 : d1);
 }
 
 // The power of two that brings a query's largest magnitude into [128, 256), and its inverse.
